@@ -119,6 +119,7 @@ def library() -> ctypes.CDLL:
         lib.bsa_decode_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.bsa_topk_pattern_static.restype = ctypes.c_int
         lib.bsa_topk_pattern_static.argtypes = [vp, vp] + [ctypes.c_int] * 6 + [vp, vp, vp]
+        long_stream._declare(lib)
         _lib = lib
     return _lib
 
@@ -443,3 +444,8 @@ def device_status(clear: bool = True) -> int:
 
 def version() -> int:
     return int(library().bsa_version())
+
+
+from . import long_stream  # noqa: E402
+from .long_stream import (Q4Cache, q4_cache, q4_decode, q4_read, q4_window_decode,  # noqa: E402,F401
+                          q4_write, stream_status, window_decode)

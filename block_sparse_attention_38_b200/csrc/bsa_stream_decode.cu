@@ -1,0 +1,963 @@
+// bsa_stream_decode.cu -- one decode step over a long cache: bf16 or 4 bits,
+// shared key/value heads, and as visible tokens either a sliding window with
+// first tokens (sinks) or the blocks of a block-CSR row.
+//
+// For each (b, cached head) the G = H / Hkv query heads of the group read the
+// same cached rows.  With x_k = scale q.k, the step gives
+// O = sum_k softmax(x)_k v_k and LSE = ln sum_k exp x_k.  It is bound by HBM:
+// 2 (d/2 + d/8) bytes a token and cached head (4 bits) or 4 d (bf16), against
+// 4 d G flops.  Both products run on the warp matrix instructions
+// (m16n8k16, fp32 accumulation) as
+//   S^T[key, head] = K Q^T         16 keys a tile, 8 heads a tile
+//   O^T[channel, head] += V^T P^T
+// so the cached rows, the large operand, fill the 16 rows of a tile and a group
+// of up to 8 heads wastes nothing.  tcgen05 would need the codes decoded into
+// shared memory or TMEM first; here they go from shared memory to the operand
+// registers with a mask and a shift.
+//
+// 4 bits (bsa_q4.cuh).  Codes enter the matrix instructions as fp16 subnormals:
+// the bits of c are the number c 2^-24, and of c << 4 the number 16 c 2^-24, so
+// two codes in place cost one AND.  Q is scaled per head by a power of two to
+// 2^13..2^14 (exact) and by 1/16 where a code is 16-fold, so the products are
+// exact; group G's sum is multiplied by the key's scale and the minimum adds
+// m_kG sum_{c in G} q_c, in fp32.  For V, P^T is multiplied by the key's scale of
+// the group before its rounding to fp16 (2^-11, against 2^-8 of the bf16
+// output), and sum_k p_k m_kG is kept in fp32.  So that small or large scales
+// lose nothing to fp16's range, the running maximum is that of
+// x_k + E - 14, with 2^E the largest scale seen (E only grows, like a maximum).
+//
+// bf16: operands by ldmatrix; P is split into two bf16 terms (P = hi + lo), so its
+// rounding costs 2^-16; the second product is free under the cache's bytes.
+//
+// Work split: a unit is 32 (16 for bf16) neighbouring cached rows.  Warps take
+// units in turn, each with its own ring of cp.async stages: no barrier or wait
+// between warps until the end.  A (b, cached head) is given to a cluster of up
+// to 8 CTAs when there are few of them; the CTAs' (max, sum, O) are joined over
+// distributed shared memory, so one launch does it all, with no workspace and
+// the same result in every run.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "bsa.h"
+#include "bsa_q4.cuh"
+
+namespace bsa {
+namespace sdec {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxM = 4096;
+
+__device__ unsigned int g_sdec_status;
+
+struct Args {
+  const __nv_bfloat16* q;       // [B, H, d]
+  const __nv_bfloat16* k_new;   // [B, Hkv, d] or null
+  const __nv_bfloat16* v_new;
+  unsigned char* k;             // bf16 rows, or codes
+  unsigned char* v;
+  unsigned char* kp;            // 4 bits: parameters
+  unsigned char* vp;
+  const int32_t* row_ptr;       // block pattern, or null: window
+  const int32_t* col_idx;
+  const int32_t* seq_len;
+  __nv_bfloat16* O;             // [B, H, d]
+  float* LSE;                   // [B, H]
+  int Hkv, G, L;
+  int chunks;                   // 8 NT-head pieces of a group
+  int cluster;
+  int bs, M;                    // block pattern
+  int window, sinks;
+  float scale_log2;
+};
+
+template <int D, bool Q4, int NT>
+struct Cfg {
+  static constexpr int GR = D / 32;
+  static constexpr int UK = Q4 ? 32 : 16;              // keys per unit
+  static constexpr int SUB = UK / 16;
+  static constexpr int ROW = Q4 ? D / 2 : 2 * D;       // bytes of a row
+  static constexpr int PROW = Q4 ? 4 * GR : 0;         // bytes of a row's parameters
+  static constexpr int V_OFF = UK * ROW;
+  static constexpr int KP_OFF = 2 * UK * ROW;
+  static constexpr int VP_OFF = KP_OFF + UK * PROW;
+  static constexpr int STAGE = 2 * UK * (ROW + PROW);  // 5 KB and 2.5 KB (4 bits), 8 and 4 KB (bf16)
+  static constexpr int STAGES = Q4 ? (D == 128 ? 2 : 3) : 3;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int HEADS = 8 * NT;
+  // overlaid on the ring at the end: each warp's O and (max, sum)
+  static constexpr int PART = kWarps * HEADS * (D + 2) * 4;
+  // the CTA's own result, read by its cluster: not overlaid
+  static constexpr int OUT = HEADS * (D + 2) * 4;
+  static constexpr int SMEM = (RING > PART ? RING : PART) + OUT;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_of(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+
+// Key (0..7) at row r of a tile's half, for the 4-bit tiles.  With it the eight
+// rows that the lanes of one load take fall into different banks, both for keys
+// (rows r, r + 1 at a time) and for values (rows 0, 2, 4, 6, then 1, 3, 5, 7).
+__device__ __forceinline__ int key_of_row(int r) { return (0x63417250u >> (4 * r)) & 7; }
+
+// Byte offset of 16-byte piece c of row r within a tile.
+template <int D, bool Q4>
+__device__ __forceinline__ int place(int r, int c) {
+  if constexpr (Q4)
+    return D == 128 ? r * 64 + ((c ^ (r & 2)) << 4) : r * 32 + (c << 4);
+  else
+    return r * 2 * D + ((c ^ (r & 7)) << 4);
+}
+
+// The rows that one (b, cached head) sees, as a list of units.
+struct Span {
+  int t;                 // newest token; -1: none
+  int units;
+  int head_units;        // window: units before the window (sinks)
+  int first_unit;        // window: the window's first unit
+  int lo, sinks;         // window: first row of the window, rows always visible
+};
+
+template <int D, bool Q4, int NT>
+struct Warp {
+  using C = Cfg<D, Q4, NT>;
+  // S^T columns 2t, 2t + 1 are this lane's heads in S and O
+  float o[D / 16][NT][4];
+  float top[NT][2];      // running maximum, log2 units (shifted by E - 14 for 4 bits)
+  float sum[NT][2];      // this lane's share of the denominator
+  float pm[Q4 ? C::GR : 1][NT][2];  // sum_k p_k m_kG, this lane's keys
+  int e;                 // exponent of the largest value scale seen
+  uint32_t qf[NT][D / 16][2];
+  float qs[Q4 ? C::GR : 1][NT][2];  // sum of q over a group, heads 2t, 2t + 1
+  float mul[NT][2];      // from accumulator to x in log2 units
+};
+
+// Query operands.  Lane 4 g + t holds head g's channels.
+template <int D, bool Q4, int NT>
+__device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long long head0, int heads,
+                                       int lane) {
+  using C = Cfg<D, Q4, NT>;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int head = nt * 8 + g;
+    const __nv_bfloat16* q = a.q + (head0 + head) * D;
+    if constexpr (Q4) {
+      uint4 raw[C::GR];
+      float amax = 0.f;
+#pragma unroll
+      for (int G = 0; G < C::GR; ++G) {
+        raw[G] = head < heads ? *reinterpret_cast<const uint4*>(q + 32 * G + 8 * t) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t r[4] = {raw[G].x, raw[G].y, raw[G].z, raw[G].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(q4::bf16lo(r[i])), fabsf(q4::bf16hi(r[i]))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;  // amax = 1.x 2^ex
+      ex = min(max(ex, -100), 116);  // both factors below stay finite
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);  // 2^(13 - ex)
+      const float mul = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 11 + ex) << 23);  // 2^(24 - 13 + ex)
+      w.mul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
+      w.mul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
+#pragma unroll
+      for (int G = 0; G < C::GR; ++G) {
+        const float v[8] = {q4::bf16lo(raw[G].x) * up, q4::bf16hi(raw[G].x) * up,
+                            q4::bf16lo(raw[G].y) * up, q4::bf16hi(raw[G].y) * up,
+                            q4::bf16lo(raw[G].z) * up, q4::bf16hi(raw[G].z) * up,
+                            q4::bf16lo(raw[G].w) * up, q4::bf16hi(raw[G].w) * up};
+        // nibbles (0, 4), (1, 5) x 1/16, (2, 6), (3, 7) x 1/16
+        w.qf[nt][2 * G][0] = pack_h(v[0], v[4]);
+        w.qf[nt][2 * G][1] = pack_h(v[1] * 0.0625f, v[5] * 0.0625f);
+        w.qf[nt][2 * G + 1][0] = pack_h(v[2], v[6]);
+        w.qf[nt][2 * G + 1][1] = pack_h(v[3] * 0.0625f, v[7] * 0.0625f);
+        float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s *= 0x1p-24f;
+        w.qs[G][nt][0] = __shfl_sync(0xffffffffu, s, 8 * t);
+        w.qs[G][nt][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w.qf[nt][kk][i] = head < heads
+                                ? *reinterpret_cast<const uint32_t*>(q + 16 * kk + 8 * i + 2 * t)
+                                : 0u;
+      w.mul[nt][0] = w.mul[nt][1] = a.scale_log2;
+    }
+  }
+}
+
+// Issues the copies of the unit that starts at cached row `row0` of the head
+// whose rows start at `base`.  Rows past the cache's end are zero-filled.
+template <int D, bool Q4, int NT>
+__device__ __forceinline__ void load_unit(const Args& a, long long base, int row0, uint32_t st,
+                                          int lane) {
+  using C = Cfg<D, Q4, NT>;
+  constexpr int PIECES = C::ROW / 16;
+#pragma unroll
+  for (int i = lane; i < C::UK * PIECES; i += 32) {
+    const int r = i / PIECES, c = i % PIECES;
+    const bool live = row0 + r < a.L;
+    const long long off = (base + (live ? row0 + r : 0)) * C::ROW + c * 16;
+    const int at = place<D, Q4>(r, c);
+    cp16(st + at, a.k + off, live);
+    cp16(st + C::V_OFF + at, a.v + off, live);
+  }
+  if constexpr (Q4) {
+    const bool live = row0 + lane < a.L;
+    const long long off = (base + (live ? row0 + lane : 0)) * C::PROW;
+    if constexpr (C::PROW == 16) {
+      cp16(st + C::KP_OFF + lane * 16, a.kp + off, live);
+      cp16(st + C::VP_OFF + lane * 16, a.vp + off, live);
+    } else {
+      cp8(st + C::KP_OFF + lane * 8, a.kp + off, live);
+      cp8(st + C::VP_OFF + lane * 8, a.vp + off, live);
+    }
+  }
+}
+
+// One warp: the new token's key and value as a cached row, for the cache itself
+// (row index `row`) or for row r of a stage.
+template <int D, bool Q4, int NT, bool TO_STAGE>
+__device__ __forceinline__ void put_new(const Args& a, long long bh, long long row, unsigned char* st,
+                                        int r, int lane) {
+  using C = Cfg<D, Q4, NT>;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const __nv_bfloat16* src = (w == 0 ? a.k_new : a.v_new) + bh * D;
+    if constexpr (Q4) {
+      uint2 raw = make_uint2(0u, 0u);
+      if (lane < D / 4) raw = *reinterpret_cast<const uint2*>(src + 4 * lane);
+      const float v[4] = {q4::bf16lo(raw.x), q4::bf16hi(raw.x), q4::bf16lo(raw.y), q4::bf16hi(raw.y)};
+      int at;
+      uint32_t par;
+      const uint32_t code = q4::quantise_row<D>(v, lane, w == 0, &at, &par);
+      const int G = lane >> 3;
+      unsigned char* cp;
+      unsigned char* pp;
+      if constexpr (TO_STAGE) {
+        cp = st + (w == 0 ? 0 : C::V_OFF) + place<D, Q4>(r, at >> 3) + (at & 7) * 2;
+        pp = st + (w == 0 ? C::KP_OFF : C::VP_OFF) + r * C::PROW + 4 * G;
+      } else {
+        cp = (w == 0 ? a.k : a.v) + row * C::ROW + at * 2;
+        pp = (w == 0 ? a.kp : a.vp) + row * C::PROW + 4 * G;
+      }
+      if (lane < D / 4) {
+        *reinterpret_cast<uint16_t*>(cp) = static_cast<uint16_t>(code);
+        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(pp) = par;
+      }
+    } else {
+      if (lane < D / 8) {
+        const uint4 raw = *reinterpret_cast<const uint4*>(src + 8 * lane);
+        unsigned char* cp;
+        if constexpr (TO_STAGE)
+          cp = st + (w == 0 ? 0 : C::V_OFF) + place<D, Q4>(r, lane);
+        else
+          cp = (w == 0 ? a.k : a.v) + row * C::ROW + lane * 16;
+        *reinterpret_cast<uint4*>(cp) = raw;
+      }
+    }
+  }
+}
+
+// Scores of a 16-key tile, S^T[key, head] * nothing yet: accumulator units.
+template <int D, bool Q4, int NT>
+__device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsigned char* st, int sub,
+                                           int lane, float (&x)[NT][4]) {
+  using C = Cfg<D, Q4, NT>;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+  if constexpr (Q4) {
+    const int r0 = sub * 16 + key_of_row(g);
+    uint32_t kw[2][C::GR], kp[2][C::GR];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i;
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(st + place<D, Q4>(r, t));
+        kw[i][0] = u.x; kw[i][1] = u.y; kw[i][2] = u.z; kw[i][3] = u.w;
+        const uint4 p = *reinterpret_cast<const uint4*>(st + C::KP_OFF + r * 16);
+        kp[i][0] = p.x; kp[i][1] = p.y; kp[i][2] = p.z; kp[i][3] = p.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(st + r * 32 + t * 8);
+        kw[i][0] = u.x; kw[i][1] = u.y;
+        const uint2 p = *reinterpret_cast<const uint2*>(st + C::KP_OFF + r * 8);
+        kp[i][0] = p.x; kp[i][1] = p.y;
+      }
+    }
+#pragma unroll
+    for (int G = 0; G < C::GR; ++G) {
+      const uint32_t u0 = kw[0][G], u1 = kw[1][G], v0 = u0 >> 8, v1 = u1 >> 8;
+      const float2 p0 = half2_of(kp[0][G]), p1 = half2_of(kp[1][G]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+                w.qf[nt][2 * G][0], w.qf[nt][2 * G][1]);
+        mma_f16(c, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u,
+                w.qf[nt][2 * G + 1][0], w.qf[nt][2 * G + 1][1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[nt][j] = fmaf(p0.x, c[j], fmaf(p0.y, w.qs[G][nt][j], x[nt][j]));
+          x[nt][2 + j] = fmaf(p1.x, c[2 + j], fmaf(p1.y, w.qs[G][nt][j], x[nt][2 + j]));
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      // matrices: keys 0-7 / 8-15 of channels 16kk.., then of channels 16kk + 8..
+      const int r = sub * 16 + (lane & 15);
+      uint32_t k[4];
+      ldmatrix4<false>(k, smem_addr(st + place<D, Q4>(r, 2 * kk + (lane >> 4))));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_bf16(x[nt], k, w.qf[nt][kk][0], w.qf[nt][kk][1]);
+    }
+  }
+}
+
+// O^T += V^T P^T for a 16-key tile; p in the layout of score_tile.
+template <int D, bool Q4, int NT>
+__device__ __forceinline__ void value_tile(Warp<D, Q4, NT>& w, const unsigned char* st, int sub, int lane,
+                                           const float (&p)[NT][4]) {
+  using C = Cfg<D, Q4, NT>;
+  const int g = lane >> 2, t = lane & 3;
+  if constexpr (Q4) {
+    const int r0 = sub * 16 + key_of_row(g);
+    const int ra = sub * 16 + key_of_row(2 * t), rb = sub * 16 + key_of_row(2 * t + 1);
+    constexpr int VW = D / 64;  // words of a lane's channels
+    uint32_t vw[4][VW], vp[2][C::GR];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ((i & 1) ? rb : ra) + 8 * (i >> 1);
+      if constexpr (D == 128) {
+        const uint2 u = *reinterpret_cast<const uint2*>(st + C::V_OFF + place<D, Q4>(r, g >> 1) + (g & 1) * 8);
+        vw[i][0] = u.x;
+        vw[i][VW - 1] = u.y;
+      } else {
+        vw[i][0] = *reinterpret_cast<const uint32_t*>(st + C::V_OFF + r * 32 + g * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i;
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(st + C::VP_OFF + r * 16);
+        vp[i][0] = u.x; vp[i][1] = u.y; vp[i][2] = u.z; vp[i][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(st + C::VP_OFF + r * 8);
+        vp[i][0] = u.x; vp[i][1] = u.y;
+      }
+    }
+#pragma unroll
+    for (int G = 0; G < C::GR; ++G) {
+      const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
+      const uint32_t e = __byte_perm(vw[0][G / 2], vw[1][G / 2], sel), e8 = e >> 8;  // keys of rows 2t, 2t + 1
+      const uint32_t f = __byte_perm(vw[2][G / 2], vw[3][G / 2], sel), f8 = f >> 8;  // the same + 8
+      const float2 s0 = half2_of(vp[0][G]), s1 = half2_of(vp[1][G]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t b0 = transpose8x8(pack_h(p[nt][0] * s0.x, p[nt][1] * s0.x));
+        const uint32_t b1 = transpose8x8(pack_h(p[nt][2] * s1.x, p[nt][3] * s1.x));
+        mma_f16(w.o[2 * G][nt], e & 0x000f000fu, e8 & 0x000f000fu, f & 0x000f000fu, f8 & 0x000f000fu, b0, b1);
+        mma_f16(w.o[2 * G + 1][nt], e & 0x00f000f0u, e8 & 0x00f000f0u, f & 0x00f000f0u, f8 & 0x00f000f0u, b0, b1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          w.pm[G][nt][j] = fmaf(p[nt][j], s0.y, fmaf(p[nt][2 + j], s1.y, w.pm[G][nt][j]));
+      }
+    }
+  } else {
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float p0 = p[nt][2 * i], p1 = p[nt][2 * i + 1];
+        const uint32_t h = pack_b(p0, p1);
+        hi[nt][i] = transpose8x8(h);
+        lo[nt][i] = transpose8x8(pack_b(p0 - q4::bf16lo(h), p1 - q4::bf16hi(h)));
+      }
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m) {
+      // transposed matrices: (channels 16m.., keys 0-7), (16m + 8.., 0-7), (16m.., 8-15), (16m + 8.., 8-15)
+      const int r = sub * 16 + (lane & 7) + ((lane >> 4) << 3);
+      uint32_t v[4];
+      ldmatrix4<true>(v, smem_addr(st + C::V_OFF + place<D, Q4>(r, 2 * m + ((lane >> 3) & 1))));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_bf16(w.o[m][nt], v, hi[nt][0], hi[nt][1]);
+        mma_bf16(w.o[m][nt], v, lo[nt][0], lo[nt][1]);
+      }
+    }
+  }
+}
+
+// Channel of O^T tile m, row half i (rows g and g + 8) of lane group g.
+template <int D, bool Q4>
+__device__ __forceinline__ int channel_of(int m, int i, int g) {
+  if constexpr (Q4)
+    return 32 * (m >> 1) + 4 * g + 2 * i + (m & 1);
+  else
+    return 16 * m + 8 * i + g;
+}
+
+template <int D, bool Q4, int NT>
+__global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_decode_kernel(const Args a) {
+  using C = Cfg<D, Q4, NT>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t bitmap[kMaxM / 32];
+  __shared__ uint16_t blocks[kMaxM];
+  __shared__ int n_blocks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int rank = static_cast<int>(blockIdx.x % a.cluster);
+  const long long grp = blockIdx.x / a.cluster;
+  const int chunk = static_cast<int>(grp % a.chunks);
+  const long long bh = grp / a.chunks;                    // (b, cached head)
+  const int b = static_cast<int>(bh / a.Hkv), hkv = static_cast<int>(bh - static_cast<long long>(b) * a.Hkv);
+  const long long base = bh * a.L;                        // cached row 0
+  const long long head0 = static_cast<long long>(b) * a.Hkv * a.G + static_cast<long long>(hkv) * a.G + chunk * C::HEADS;
+  const int heads = min(C::HEADS, a.G - chunk * C::HEADS);
+
+  int len = a.seq_len[b];
+  if (len < 0 || len > a.L) {
+    if (tid == 0) atomicOr(&g_sdec_status, BSA_STATUS_BAD_SEQ_LEN);
+    len = 0;
+  }
+  Span sp;
+  sp.t = len - 1;
+  sp.units = sp.head_units = sp.first_unit = sp.lo = sp.sinks = 0;
+  if (len > 0 && a.row_ptr == nullptr) {
+    sp.lo = a.window < len ? len - a.window : 0;
+    sp.sinks = a.sinks;
+    sp.first_unit = sp.lo / C::UK;
+    sp.head_units = min((min(a.sinks, sp.lo) + C::UK - 1) / C::UK, sp.first_unit);
+    sp.units = sp.head_units + sp.t / C::UK + 1 - sp.first_unit;
+  } else if (len > 0) {
+    const int i = sp.t / a.bs, W = i / 32 + 1;
+    for (int w = tid; w < W; w += kThreads) bitmap[w] = 0u;
+    __syncthreads();
+    int e0 = a.row_ptr[static_cast<long long>(hkv) * a.M + i];
+    int e1 = a.row_ptr[static_cast<long long>(hkv) * a.M + i + 1];
+    if (e0 < 0 || e1 < e0) {
+      if (tid == 0) atomicOr(&g_sdec_status, BSA_STATUS_BAD_ROW_PTR);
+      e0 = e1 = 0;
+    }
+    for (int e = e0 + tid; e < e1; e += kThreads) {
+      const int j = a.col_idx[e];
+      if (j < 0 || j >= a.M)
+        atomicOr(&g_sdec_status, BSA_STATUS_BAD_COLUMN);
+      else if (j <= i)
+        atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+    }
+    __syncthreads();
+    if (warp == 0) {  // the blocks in ascending order
+      int n = 0;
+      for (int w0 = 0; w0 < W; w0 += 32) {
+        uint32_t bits = w0 + lane < W ? bitmap[w0 + lane] : 0u;
+        int at = __popc(bits);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += y;
+        }
+        const int total = __shfl_sync(0xffffffffu, at, 31);
+        at += n - __popc(bits);
+        for (; bits; bits &= bits - 1) blocks[at++] = static_cast<uint16_t>((w0 + lane) * 32 + __ffs(bits) - 1);
+        n += total;
+      }
+      if (lane == 0) n_blocks = n;
+    }
+    __syncthreads();
+    // every block is bs rows; of the newest token's block, the rows up to it
+    const int nb = n_blocks;
+    sp.units = nb * (a.bs / C::UK);
+    if (nb > 0 && blocks[nb - 1] == i) sp.units -= a.bs / C::UK - ((sp.t - i * a.bs) / C::UK + 1);
+  }
+  auto row_of = [&](int u) {  // first cached row of unit u
+    if (a.row_ptr == nullptr)
+      return (u < sp.head_units ? u : sp.first_unit + u - sp.head_units) * C::UK;
+    const int per = a.bs / C::UK;
+    return blocks[u / per] * a.bs + (u % per) * C::UK;
+  };
+
+  Warp<D, Q4, NT> w;
+  load_q<D, Q4, NT>(w, a, head0, heads, lane);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w.top[nt][j] = -INFINITY;
+      w.sum[nt][j] = 0.f;
+#pragma unroll
+      for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] = 0.f;
+    }
+  w.e = -100;
+#pragma unroll
+  for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.o[m][nt][i] = 0.f;
+
+  // The new token's row goes into the cache once; the warp that attends to it
+  // takes it from k_new / v_new again, so no order between the two is needed.
+  if (a.k_new != nullptr && len > 0 && rank == 0 && chunk == 0 && warp == kWarps - 1)
+    put_new<D, Q4, NT, false>(a, bh, base + sp.t, nullptr, 0, lane);
+
+  unsigned char* ring = smem + warp * C::STAGES * C::STAGE;
+  const uint32_t ring_u = smem_addr(ring);
+  const int step = a.cluster * kWarps;
+  const int u0 = warp * a.cluster + rank;
+  {
+    int u = u0;
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s, u += step) {
+      if (u < sp.units) load_unit<D, Q4, NT>(a, base, row_of(u), ring_u + s * C::STAGE, lane);
+      cp_commit();
+    }
+  }
+  int slot = 0;
+  for (int u = u0; u < sp.units; u += step) {
+    {
+      const int un = u + (C::STAGES - 1) * step;
+      int sn = slot + C::STAGES - 1;
+      if (sn >= C::STAGES) sn -= C::STAGES;
+      if (un < sp.units) load_unit<D, Q4, NT>(a, base, row_of(un), ring_u + sn * C::STAGE, lane);
+      cp_commit();
+    }
+    cp_wait<C::STAGES - 1>();
+    __syncwarp();
+    unsigned char* st = ring + slot * C::STAGE;
+    const int row0 = row_of(u);
+    bool all;  // every row of the unit is visible
+    if (a.row_ptr == nullptr)
+      all = row0 + C::UK - 1 <= sp.t && (row0 >= sp.lo || row0 + C::UK <= sp.sinks);
+    else
+      all = row0 + C::UK - 1 <= sp.t;
+    auto visible = [&](int r) {
+      const int k = row0 + r;
+      return k <= sp.t && (a.row_ptr != nullptr || k >= sp.lo || k < sp.sinks);
+    };
+    if (!all || (a.k_new != nullptr && row0 + C::UK - 1 == sp.t)) {
+      if (a.k_new != nullptr && row0 <= sp.t && sp.t < row0 + C::UK) {
+        put_new<D, Q4, NT, true>(a, bh, 0, st, sp.t - row0, lane);
+        __syncwarp();
+      }
+      // Hidden rows take weight 0, but 0 times what they hold (anything, NaN
+      // too) must be 0: their values are cleared.
+      for (int r = lane; r < C::UK; r += 32)
+        if (!visible(r)) {
+          if constexpr (Q4) {
+#pragma unroll
+            for (int G = 0; G < C::GR; ++G)
+              *reinterpret_cast<uint32_t*>(st + C::VP_OFF + r * C::PROW + 4 * G) = 0u;
+          } else {
+            for (int c = 0; c < C::ROW / 16; ++c)
+              *reinterpret_cast<uint4*>(st + C::V_OFF + r * C::ROW + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+      __syncwarp();
+    }
+
+    float x[C::SUB][NT][4];
+#pragma unroll
+    for (int s = 0; s < C::SUB; ++s) score_tile<D, Q4, NT>(w, st, s, lane, x[s]);
+#pragma unroll
+    for (int s = 0; s < C::SUB; ++s)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[s][nt][i] *= w.mul[nt][i & 1];
+    if (!all) {
+#pragma unroll
+      for (int s = 0; s < C::SUB; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = s * 16 + 8 * i + (Q4 ? key_of_row(g) : g);
+          if (!visible(r)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[s][nt][2 * i] = x[s][nt][2 * i + 1] = -INFINITY;
+          }
+        }
+    }
+    // exponent of the unit's largest value scale
+    float shift = 0.f;
+    if constexpr (Q4) {
+      const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + C::VP_OFF + lane * C::PROW);
+      uint32_t big = 0u;
+#pragma unroll
+      for (int G = 0; G < C::GR; ++G) big = max(big, vp[G] & 0x7fffu);
+      big = __reduce_max_sync(0xffffffffu, big);
+      w.e = max(w.e, static_cast<int>(big >> 10) - 15);
+      shift = static_cast<float>(w.e - 14);
+    }
+    float grow[NT][2];
+    bool any = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < C::SUB; ++s) m = fmaxf(m, fmaxf(x[s][nt][j], x[s][nt][2 + j]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m += shift;
+        const float old = w.top[nt][j];
+        // never below the old shifted maximum by more than E grew: P stays in range
+        const float now = fmaxf(old, m);
+        grow[nt][j] = now == old ? 1.f : ex2(old - now);
+        any |= now != old;
+        w.top[nt][j] = now;
+      }
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          w.sum[nt][j] *= grow[nt][j];
+#pragma unroll
+          for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] *= grow[nt][j];
+#pragma unroll
+          for (int m = 0; m < D / 16; ++m) {
+            w.o[m][nt][j] *= grow[nt][j];
+            w.o[m][nt][2 + j] *= grow[nt][j];
+          }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < C::SUB; ++s) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float top = w.top[nt][i & 1];
+          const float p = ex2(x[s][nt][i] - (top == -INFINITY ? 0.f : top));
+          x[s][nt][i] = p;
+          w.sum[nt][i & 1] += p;
+        }
+      value_tile<D, Q4, NT>(w, st, s, lane, x[s]);
+    }
+    __syncwarp();  // the stage is free for the next copy
+    if (++slot == C::STAGES) slot = 0;
+  }
+  cp_wait<0>();
+  __syncthreads();  // the ring becomes the warps' partial results
+
+  // ------------------------------------------------------------------ join
+  float* part = reinterpret_cast<float*>(smem) + warp * C::HEADS * (D + 2);  // O [head][D], then max, sum
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float sum = w.sum[nt][j];
+      float pm[Q4 ? C::GR : 1];
+#pragma unroll
+      for (int G = 0; G < (Q4 ? C::GR : 1); ++G) pm[G] = w.pm[G][nt][j];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if constexpr (Q4) {
+#pragma unroll
+          for (int G = 0; G < C::GR; ++G) pm[G] += __shfl_xor_sync(0xffffffffu, pm[G], o);
+        }
+      }
+      const int head = nt * 8 + 2 * t4 + j;
+      if (g == 0) {
+        part[C::HEADS * D + head] = w.top[nt][j];
+        part[C::HEADS * D + C::HEADS + head] = sum;
+      }
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = w.o[m][nt][2 * i + j];
+          if constexpr (Q4) v = fmaf(v, (m & 1) ? 0x1p20f : 0x1p24f, pm[m >> 1]);
+          part[head * D + channel_of<D, Q4>(m, i, g)] = v;
+        }
+    }
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem + C::SMEM - C::OUT);
+  const float* parts = reinterpret_cast<const float*>(smem);
+  constexpr int PS = C::HEADS * (D + 2);
+  for (int e = tid; e < heads * D; e += kThreads) {
+    const int head = e / D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, parts[v * PS + C::HEADS * D + head]);
+    float o = 0.f, sum = 0.f;
+    if (top != -INFINITY) {
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float m = parts[v * PS + C::HEADS * D + head];
+        if (m != -INFINITY) {
+          const float f = ex2(m - top);
+          o = fmaf(parts[v * PS + e], f, o);
+          sum = fmaf(parts[v * PS + C::HEADS * D + C::HEADS + head], f, sum);
+        }
+      }
+    }
+    if (a.cluster == 1) {
+      a.O[head0 * D + e] = __float2bfloat16_rn(top == -INFINITY ? 0.f : o / sum);
+      if (e % D == 0)
+        a.LSE[head0 + head] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    } else {
+      out[e] = o;
+      if (e % D == 0) {
+        out[C::HEADS * D + head] = top;
+        out[C::HEADS * D + C::HEADS + head] = sum;
+      }
+    }
+  }
+  if (a.cluster == 1) return;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  const int n = a.cluster;
+  for (int e = rank * kThreads + tid; e < heads * D; e += n * kThreads) {
+    const int head = e / D;
+    float top = -INFINITY;
+    for (int v = 0; v < n; ++v) top = fmaxf(top, cluster.map_shared_rank(out, v)[C::HEADS * D + head]);
+    float o = 0.f, sum = 0.f;
+    if (top != -INFINITY)
+      for (int v = 0; v < n; ++v) {
+        const float* q = cluster.map_shared_rank(out, v);
+        const float m = q[C::HEADS * D + head];
+        if (m != -INFINITY) {
+          const float f = ex2(m - top);
+          o = fmaf(q[e], f, o);
+          sum = fmaf(q[C::HEADS * D + C::HEADS + head], f, sum);
+        }
+      }
+    a.O[head0 * D + e] = __float2bfloat16_rn(top == -INFINITY ? 0.f : o / sum);
+    if (e % D == 0)
+      a.LSE[head0 + head] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  cluster.sync();  // no CTA leaves while another reads its result
+}
+
+template <int D, bool Q4, int NT>
+int launch(Args a, long long groups, long long max_units, cudaStream_t s) {
+  using C = Cfg<D, Q4, NT>;
+  const auto kernel = stream_decode_kernel<D, Q4, NT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  // CTAs per (b, cached head): enough to cover the SMs twice, while a warp
+  // keeps two units or more.
+  int n = 1;
+  while (n < 8 && groups * n < 2 * 148 && max_units > 2LL * kWarps * n) n *= 2;
+  a.cluster = n;
+  const long long blocks = groups * n;
+  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = n;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return BSA_ERR_CUDA;
+  }
+  return BSA_OK;
+}
+
+template <bool Q4>
+int dispatch(Args a, int B, int d, long long max_units, cudaStream_t s) {
+  const int nt = a.G > 8 ? 2 : 1;
+  a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
+  const long long groups = static_cast<long long>(B) * a.Hkv * a.chunks;
+  if (d == 64) return nt == 1 ? launch<64, Q4, 1>(a, groups, max_units, s) : launch<64, Q4, 2>(a, groups, max_units, s);
+  return nt == 1 ? launch<128, Q4, 1>(a, groups, max_units, s) : launch<128, Q4, 2>(a, groups, max_units, s);
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The checks that every step shares; fills what they cover.
+int common(Args* a, const void* q, const void* k_new, const void* v_new, const int32_t* seq_len, int B,
+           int H, int Hkv, int L, int d, float scale, void* O, float* LSE) {
+  if (!q || !seq_len || !O || !LSE || (k_new == nullptr) != (v_new == nullptr)) return BSA_ERR_INVALID_ARG;
+  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0 || !std::isfinite(scale))
+    return BSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(O) || (k_new && (!aligned16(k_new) || !aligned16(v_new))) ||
+      (reinterpret_cast<uintptr_t>(LSE) & 3u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  *a = Args{};
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a->v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a->seq_len = seq_len;
+  a->O = static_cast<__nv_bfloat16*>(O);
+  a->LSE = LSE;
+  a->Hkv = Hkv;
+  a->G = H / Hkv;
+  a->L = L;
+  a->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  return BSA_OK;
+}
+
+int set_cache(Args* a, const bsa_q4_cache* c) {
+  if (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) || !aligned16(c->v_params))
+    return BSA_ERR_INVALID_ARG;
+  a->k = static_cast<unsigned char*>(c->k_codes);
+  a->v = static_cast<unsigned char*>(c->v_codes);
+  a->kp = static_cast<unsigned char*>(c->k_params);
+  a->vp = static_cast<unsigned char*>(c->v_params);
+  return BSA_OK;
+}
+
+long long window_units(int L, int window, int sinks, int unit) {
+  const long long near = window < L ? window : L, far = sinks < L ? sinks : L;
+  return (near + far + 2 * unit - 1) / unit;
+}
+
+}  // namespace sdec
+
+int take_status(const void* symbol, uint32_t* status, int clear);
+int stream_decode_status(uint32_t* status, int clear) {
+  return take_status(&sdec::g_sdec_status, status, clear);
+}
+}  // namespace bsa
+
+extern "C" int bsa_q4_decode(const void* q, const void* k_new, const void* v_new,
+                             const bsa_q4_cache* cache, const int32_t* row_ptr,
+                             const int32_t* col_idx, const int32_t* seq_len, int H, int block_size,
+                             float scale, void* O, float* LSE, void* stream) {
+  using namespace bsa::sdec;
+  if (!cache || !row_ptr || !col_idx || block_size < 1) return BSA_ERR_INVALID_ARG;
+  Args a;
+  int rc = common(&a, q, k_new, v_new, seq_len, cache->B, H, cache->H, cache->L, cache->d, scale, O, LSE);
+  if (rc == BSA_OK || rc == BSA_ERR_UNSUPPORTED) {
+    const int bad = set_cache(&a, cache);
+    if (bad != BSA_OK) return bad;
+  }
+  if (rc != BSA_OK) return rc;
+  if (cache->L % block_size != 0) return BSA_ERR_INVALID_ARG;
+  if (block_size != 32 && block_size != 64 && block_size != 128) return BSA_ERR_UNSUPPORTED;
+  if (cache->L / block_size > kMaxM) return BSA_ERR_UNSUPPORTED;
+  a.row_ptr = row_ptr;
+  a.col_idx = col_idx;
+  a.bs = block_size;
+  a.M = cache->L / block_size;
+  if (static_cast<long long>(a.Hkv) * a.M + 1 > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  return dispatch<true>(a, cache->B, cache->d, cache->L / 32, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int bsa_q4_window_decode(const void* q, const void* k_new, const void* v_new,
+                                    const bsa_q4_cache* cache, const int32_t* seq_len, int H, int window,
+                                    int sinks, float scale, void* O, float* LSE, void* stream) {
+  using namespace bsa::sdec;
+  if (!cache || window < 1 || sinks < 0) return BSA_ERR_INVALID_ARG;
+  Args a;
+  int rc = common(&a, q, k_new, v_new, seq_len, cache->B, H, cache->H, cache->L, cache->d, scale, O, LSE);
+  if (rc == BSA_OK || rc == BSA_ERR_UNSUPPORTED) {
+    const int bad = set_cache(&a, cache);
+    if (bad != BSA_OK) return bad;
+  }
+  if (rc != BSA_OK) return rc;
+  a.window = window;
+  a.sinks = sinks;
+  return dispatch<true>(a, cache->B, cache->d, window_units(cache->L, window, sinks, 32),
+                        static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int bsa_window_decode(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                 void* v_cache, const int32_t* seq_len, int B, int H, int Hkv, int L, int d,
+                                 int window, int sinks, float scale, void* O, float* LSE, void* stream) {
+  using namespace bsa::sdec;
+  if (!k_cache || !v_cache || window < 1 || sinks < 0) return BSA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return BSA_ERR_INVALID_ARG;
+  Args a;
+  const int rc = common(&a, q, k_new, v_new, seq_len, B, H, Hkv, L, d, scale, O, LSE);
+  if (rc != BSA_OK) return rc;
+  a.k = static_cast<unsigned char*>(k_cache);
+  a.v = static_cast<unsigned char*>(v_cache);
+  a.window = window;
+  a.sinks = sinks;
+  return dispatch<false>(a, B, d, window_units(L, window, sinks, 16), static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,247 @@
+"""Long streams: a key/value cache held in 4 bits and decode steps over long
+caches, with a sliding window and first tokens that stay visible (sinks) or
+with a block pattern.  Marshalling only, as in the rest of the binding; the
+functions are those of the last section of include/bsa.h.
+
+H query heads share Hkv cached heads: query head h reads cached head
+h // (H // Hkv).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple, Optional
+
+from . import BsaError, _check, library  # noqa: F401  (defined before this module is imported)
+
+_i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", _vp), ("stride_b", _i64), ("stride_h", _i64), ("stride_n", _i64)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_params", _vp), ("v_codes", _vp), ("v_params", _vp),
+                ("B", _i32), ("H", _i32), ("L", _i32), ("d", _i32)]
+
+
+def _declare(lib) -> None:
+    """Argument types of this module's entry points (called once by library())."""
+    i, f, view, cache = ctypes.c_int, ctypes.c_float, ctypes.POINTER(_View), ctypes.POINTER(_Cache)
+    for name, types in (
+            ("bsa_q4_write", [cache, view, view, _vp, _vp, i, _vp]),
+            ("bsa_q4_read", [cache, _vp, _vp, i, _vp, _vp, _vp]),
+            ("bsa_q4_decode", [_vp, _vp, _vp, cache, _vp, _vp, _vp, i, i, f, _vp, _vp, _vp]),
+            ("bsa_q4_window_decode", [_vp, _vp, _vp, cache, _vp, i, i, i, f, _vp, _vp, _vp]),
+            ("bsa_window_decode", [_vp] * 6 + [i] * 7 + [f, _vp, _vp, _vp]),
+            ("bsa_stream_status", [ctypes.POINTER(ctypes.c_uint32), i])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, types
+
+
+class Q4Cache(NamedTuple):
+    """The four tensors of a 4-bit cache of Hkv heads: codes uint8 [B, Hkv, L, d/2]
+    and parameters fp16 [B, Hkv, L, d/32, 2] (scale, minimum), for keys and values."""
+
+    k_codes: "torch.Tensor"  # noqa: F821
+    k_params: "torch.Tensor"  # noqa: F821
+    v_codes: "torch.Tensor"  # noqa: F821
+    v_params: "torch.Tensor"  # noqa: F821
+
+
+def q4_cache(B: int, Hkv: int, L: int, d: int, device="cuda") -> Q4Cache:
+    """A 4-bit cache with room for L tokens of B sequences; every row reads back as 0."""
+    import torch
+
+    def codes():
+        return torch.zeros((B, Hkv, L, d // 2), dtype=torch.uint8, device=device)
+
+    def params():
+        return torch.zeros((B, Hkv, L, d // 32, 2), dtype=torch.float16, device=device)
+
+    return Q4Cache(codes(), params(), codes(), params())
+
+
+def _ints(name, t, n, device):
+    import torch
+
+    if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def _cache_arg(cache):
+    """(ctypes struct, B, Hkv, L, d, device) of a checked Q4Cache."""
+    import torch
+
+    kc, kp, vc, vp = cache
+    if kc.dim() != 4:
+        raise ValueError("k_codes must be [B, Hkv, L, d/2]")
+    B, H, L, half = kc.shape
+    device = kc.device
+    if kc.shape != vc.shape or kp.shape != (B, H, L, half // 16, 2) or vp.shape != kp.shape:
+        raise ValueError("the cache's tensors must be codes [B, Hkv, L, d/2] and parameters "
+                         "[B, Hkv, L, d/32, 2], alike for keys and values")
+    for t, dtype in ((kc, torch.uint8), (vc, torch.uint8), (kp, torch.float16), (vp, torch.float16)):
+        if not t.is_cuda or t.device != device or t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError("the cache's tensors must be contiguous CUDA tensors on one device, "
+                             "codes uint8 and parameters fp16")
+    arg = _Cache(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, H, L, 2 * half)
+    return arg, B, H, L, 2 * half, device
+
+
+def _view(name, t, shape, device):
+    """bsa_view of a bf16 tensor whose last dimension is contiguous."""
+    import torch
+
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_cuda or t.device != device or t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor on {device}")
+    sb, sh, sn, sd = t.stride()
+    # the stride of a dimension of one entry is never used
+    sb, sh, sn = (0 if shape[0] == 1 else sb, 0 if shape[1] == 1 else sh, 0 if shape[2] == 1 else sn)
+    if sd != 1 or sb % 8 or sh % 8 or sn % 8:
+        raise ValueError(f"{name} must have a contiguous last dimension and other strides that are "
+                         "multiples of 8")
+    return _View(t.data_ptr(), sb, sh, sn)
+
+
+def _rows(name, t, shape, device, dtype):
+    if tuple(t.shape) != shape or t.device != device or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _call(device, name, *args):
+    """The library function `name` with `device` current, on its current stream."""
+    import torch
+
+    stream = torch.cuda.current_stream(device).cuda_stream
+    fn = getattr(library(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc:
+        _check(rc, name)
+
+
+def q4_write(cache: Q4Cache, k, v, start, lens=None) -> None:
+    """Quantises rows into the cache (bsa_q4_write): row i of k, v (CUDA bf16
+    [B, Hkv, T, d], any strides that are multiples of 8 with d contiguous)
+    becomes cached row start[b] + i, for i < lens[b] (T where lens is None).
+
+    start, lens: CUDA int32 [B].  One token of each sequence is T = 1 with
+    start its position; other cached rows stay as they were.
+    """
+    arg, B, H, L, d, device = _cache_arg(cache)
+    if k.dim() != 4:
+        raise ValueError("k, v must be [B, Hkv, T, d]")
+    shape = (B, H, int(k.shape[2]), d)
+    kv, vv = _view("k", k, shape, device), _view("v", v, shape, device)
+    _call(device, "bsa_q4_write", arg, kv, vv, _ints("start", start, B, device),
+          None if lens is None else _ints("lens", lens, B, device), shape[2])
+
+
+def q4_read(cache: Q4Cache, start, T: int, lens=None, out=None):
+    """The cached rows start[b] .. start[b] + T - 1 as bf16 (k, v), each
+    [B, Hkv, T, d] contiguous (bsa_q4_read); rows from lens[b] on are zero.
+
+    out: a pair of tensors to write into.
+    """
+    import torch
+
+    arg, B, H, L, d, device = _cache_arg(cache)
+    shape = (B, H, int(T), d)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=device),
+               torch.empty(shape, dtype=torch.bfloat16, device=device))
+    k, v = out
+    _call(device, "bsa_q4_read", arg, _ints("start", start, B, device),
+          None if lens is None else _ints("lens", lens, B, device), shape[2],
+          _rows("out k", k, shape, device, torch.bfloat16), _rows("out v", v, shape, device, torch.bfloat16))
+    return k, v
+
+
+def _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse):
+    """Checked pieces every decode step shares: (q, k_new, v_new pointers, H, scale, O, LSE)."""
+    import torch
+
+    bf16 = torch.bfloat16
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % Hkv:
+        raise ValueError("q must be [B, H, d] with the cache's B and d, and H a multiple of its heads")
+    H = int(q.shape[1])
+    if (k_new is None) != (v_new is None):
+        raise ValueError("give both k_new and v_new, or neither")
+    qp = _rows("q", q, (B, H, d), device, bf16)
+    kn = vn = None
+    if k_new is not None:
+        kn, vn = (_rows(n, t, (B, Hkv, d), device, bf16) for n, t in (("k_new", k_new), ("v_new", v_new)))
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=device)
+    _rows("out", out, (B, H, d), device, bf16)
+    _rows("lse", lse, (B, H), device, torch.float32)
+    return qp, kn, vn, H, 1.0 / math.sqrt(d) if scale is None else float(scale), out, lse
+
+
+def q4_decode(q, cache: Q4Cache, seq_len, row_ptr, col_idx, block_size: int, scale: Optional[float] = None,
+              k_new=None, v_new=None, out=None, lse=None):
+    """One decode step over a 4-bit cache by a block pattern (bsa_q4_decode).
+
+    q: CUDA bf16 [B, H, d]; seq_len: CUDA int32 [B], tokens including the new
+    one; row_ptr, col_idx: CUDA int32 block-CSR over the cached heads' L //
+    block_size block rows.  With k_new, v_new (bf16 [B, Hkv, d]) the new token is
+    quantised into row seq_len[b] - 1 first.  Returns (O bf16 [B, H, d], LSE
+    fp32 [B, H]).
+    """
+    arg, B, Hkv, L, d, device = _cache_arg(cache)
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
+    rp = _ints("row_ptr", row_ptr, Hkv * (L // int(block_size)) + 1, device)
+    ci = _ints("col_idx", col_idx, col_idx.numel(), device) if col_idx.numel() else rp
+    _call(device, "bsa_q4_decode", qp, kn, vn, arg, rp, ci, _ints("seq_len", seq_len, B, device), H,
+          int(block_size), scale, out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def q4_window_decode(q, cache: Q4Cache, seq_len, window: int, sinks: int = 0, scale: Optional[float] = None,
+                     k_new=None, v_new=None, out=None, lse=None):
+    """One decode step over a 4-bit cache with a sliding window (bsa_q4_window_decode):
+    the rows k <= t = seq_len[b] - 1 with k > t - window or k < sinks; window >= L
+    sees every row.  Arguments and result as `q4_decode`."""
+    arg, B, Hkv, L, d, device = _cache_arg(cache)
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
+    _call(device, "bsa_q4_window_decode", qp, kn, vn, arg, _ints("seq_len", seq_len, B, device), H, int(window),
+          int(sinks), scale, out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int = 0, scale: Optional[float] = None,
+                  k_new=None, v_new=None, out=None, lse=None):
+    """One decode step over a bf16 cache [B, Hkv, L, d] with a sliding window
+    (bsa_window_decode); arguments and result as `q4_window_decode`."""
+    import torch
+
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [B, Hkv, L, d]")
+    B, Hkv, L, d = (int(x) for x in k_cache.shape)
+    device = k_cache.device
+    if not k_cache.is_cuda:
+        raise ValueError("the caches must be CUDA tensors")
+    kc, vc = (_rows(n, t, (B, Hkv, L, d), device, torch.bfloat16)
+              for n, t in (("k_cache", k_cache), ("v_cache", v_cache)))
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
+    _call(device, "bsa_window_decode", qp, kn, vn, kc, vc, _ints("seq_len", seq_len, B, device), B, H, Hkv, L, d,
+          int(window), int(sinks), scale, out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def stream_status(clear: bool = True) -> int:
+    """OR of STATUS_* bits raised by this module's kernels on the current device (synchronises it)."""
+    v = ctypes.c_uint32(0)
+    _check(library().bsa_stream_status(ctypes.byref(v), int(bool(clear))), "bsa_stream_status")
+    return int(v.value)

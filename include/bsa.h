@@ -1,7 +1,8 @@
 /*
  * bsa.h -- C ABI of the B200 block-sparse attention library: the host
  * pattern builder, the forward, and for the same patterns the backward pass,
- * a decode step over a KV cache and content-based top-k block selection.
+ * a decode step over a KV cache and content-based top-k block selection; and
+ * for long streams a 4-bit KV cache and sliding-window attention.
  *
  * The forward computes O = softmax(scale * Q K^T) V in which every query
  * row's softmax covers only the key blocks that its block row selects
@@ -360,6 +361,102 @@ int bsa_decode(const void* q, const void* k_new, const void* v_new, void* k_cach
 /* bsa_decode_status -- as bsa_device_status, for the status word the decode
  * kernel sets (BSA_STATUS_TIMEOUT, _BAD_COLUMN, _BAD_ROW_PTR, _BAD_SEQ_LEN). */
 int bsa_decode_status(uint32_t* status, int clear);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Long streams: a key/value cache held in 4 bits, and decode steps over it or
+ * over a bf16 cache, with a sliding window and first tokens that stay visible
+ * (sinks) or with a block pattern.  Here H query heads share Hkv cached heads
+ * (H a multiple of Hkv; query head h reads cached head h / (H / Hkv)).
+ * ---------------------------------------------------------------------------
+ *
+ * The 4-bit cache.  A row of d channels (the key or the value of one token and
+ * cached head) is cut into groups of 32 channels.  A group stores a scale
+ * s = fp16((max - min) / 15) and a minimum m = fp16(min), the quotient taken in
+ * fp32 and both limited to +-65504, and a code floor((x - m) / s + 1/2) in 0..15
+ * for each channel (0 where s is 0); it reads back as code * s + m.  A group
+ * that holds a NaN reads back as NaN; an infinity is limited like the rest.
+ *
+ * k_codes, v_codes: device bytes [B, H, L, d/2]; k_params, v_params: device
+ * fp16 [B, H, L, d/32, 2] (scale, minimum); all contiguous, 16-byte aligned,
+ * H the number of cached heads.  Order within a row (codes are 4 bits, lower
+ * nibble first): keys, 32-bit word t * (d/32) + g holds channels 32g + 8t .. +7;
+ * values, 16-bit piece y * (d/32) + g holds channels 32g + 4y .. +3.
+ */
+typedef struct {
+  void* k_codes;
+  void* k_params;
+  void* v_codes;
+  void* v_params;
+  int32_t B, H, L, d;
+} bsa_q4_cache;
+
+/* A bf16 tensor [B, H, N, d] with its own strides, in elements; d is
+ * contiguous, the data 16-byte aligned, every stride a multiple of 8. */
+typedef struct {
+  const void* data;
+  int64_t stride_b, stride_h, stride_n;
+} bsa_view;
+
+/*
+ * bsa_q4_write -- quantises rows as they enter the cache: row i of k and v
+ * ([B, H, T, d] views) becomes cached row start[b] + i, for i < lens[b].
+ * start, lens: device int32 [B]; lens NULL: T rows each.  One token is T = 1 with
+ * start = its position.  Cached rows outside those ranges are left as they were.
+ * A range that is not within [0, L), or lens[b] outside [0, T], sets
+ * BSA_STATUS_BAD_SEQ_LEN and writes nothing for that b.
+ * Supported: d in {64, 128}.  Nothing allocated or synchronised; errors as
+ * everywhere.
+ */
+int bsa_q4_write(const bsa_q4_cache* cache, const bsa_view* k, const bsa_view* v,
+                 const int32_t* start, const int32_t* lens, int T, void* stream);
+
+/*
+ * bsa_q4_read -- the values that cached rows start[b] .. start[b] + lens[b] - 1
+ * stand for, rounded to bf16, into k and v (device bf16 [B, H, T, d]
+ * contiguous, 16-byte aligned).  Output rows from lens[b] to T are set to zero,
+ * and all of them where the range is bad (reported as for bsa_q4_write).
+ */
+int bsa_q4_read(const bsa_q4_cache* cache, const int32_t* start, const int32_t* lens, int T, void* k,
+                void* v, void* stream);
+
+/*
+ * One decode step for each query head: the new token of entry b sits at
+ * t = seq_len[b] - 1, O = sum softmax(scale q.k) v over the rows it sees, LSE
+ * the natural log-sum-exp of the scaled scores; no rows gives O = 0, LSE = -inf.
+ *
+ *  bsa_q4_decode         the rows <= t of the blocks j <= t / block_size that
+ *                        row t / block_size of the cached head lists in a
+ *                        block-CSR over [Hkv * M] rows, M = L / block_size (a
+ *                        row is a set, as for bsa_decode);
+ *  bsa_q4_window_decode  the rows k <= t with k > t - window or k < sinks
+ *                        (window >= L: every row);
+ *  bsa_window_decode     the same over a bf16 cache [B, Hkv, L, d].
+ *
+ * q: device bf16 [B, H, d]; k_new, v_new: device bf16 [B, Hkv, d] or both NULL.
+ * With them the step first puts the new token into cached row t (quantised for
+ * a 4-bit cache) and attends to it as cached; else row t must hold it.  Cached
+ * rows that are not visible may hold anything: they never reach the result.
+ * seq_len: device int32 [B] in 0..L (0: an empty entry, nothing appended);
+ * others set BSA_STATUS_BAD_SEQ_LEN and count as 0.  O: bf16 [B, H, d]; LSE:
+ * fp32 [B, H].  16-byte aligned (LSE 4).  One launch, enqueued on `stream`;
+ * no workspace, nothing allocated or synchronised, and the same bits every run.
+ * Supported: d in {64, 128}; any H / Hkv; block_size in {32, 64, 128} with
+ * L % block_size == 0 and M <= 4096 (bsa_q4_decode only).
+ */
+int bsa_q4_decode(const void* q, const void* k_new, const void* v_new, const bsa_q4_cache* cache,
+                  const int32_t* row_ptr, const int32_t* col_idx, const int32_t* seq_len, int H,
+                  int block_size, float scale, void* O, float* LSE, void* stream);
+int bsa_q4_window_decode(const void* q, const void* k_new, const void* v_new, const bsa_q4_cache* cache,
+                         const int32_t* seq_len, int H, int window, int sinks, float scale, void* O,
+                         float* LSE, void* stream);
+int bsa_window_decode(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                      const int32_t* seq_len, int B, int H, int Hkv, int L, int d, int window, int sinks,
+                      float scale, void* O, float* LSE, void* stream);
+
+/* bsa_stream_status -- as bsa_device_status, for the status words of the
+ * functions of this section. */
+int bsa_stream_status(uint32_t* status, int clear);
 
 /*
  * bsa_device_status -- read (and with clear != 0, reset) the status word of
