@@ -6,7 +6,8 @@ The library holds the host pattern builder (bsa_pattern.cpp) and the CUDA
 translation units: the forward launcher with its kernel (bsa_forward.cu),
 top-k block selection (bsa_topk.cu), the decode step (bsa_decode.cu), the
 backward pass (bsa_backward.cu), the 4-bit cache (bsa_q4_cache.cu) and the
-decode steps over long caches (bsa_stream_decode.cu).  CUDA runtime is linked
+decode steps over long caches (bsa_stream_decode.cu) and sliding-window
+attention (bsa_window_fwd.cu).  CUDA runtime is linked
 statically; the driver's tensor-map encoder is looked up at run time, so the
 library loads on a machine without a GPU (only compute calls need one).
 """
@@ -23,7 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "bsa_pattern.cpp"), os.path.join(CSRC, "bsa_forward.cu"),
            os.path.join(CSRC, "bsa_topk.cu"), os.path.join(CSRC, "bsa_decode.cu"),
            os.path.join(CSRC, "bsa_backward.cu"), os.path.join(CSRC, "bsa_q4_cache.cu"),
-           os.path.join(CSRC, "bsa_stream_decode.cu")]
+           os.path.join(CSRC, "bsa_stream_decode.cu"), os.path.join(CSRC, "bsa_window_fwd.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "bsa.h")]
 LIB = os.path.join(HERE, "libbsa.so")
@@ -31,7 +32,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17",
+    "--threads", "0", "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-I" + os.path.join(ROOT, "include"),

@@ -1,0 +1,585 @@
+// bsa_window_fwd.cu -- attention with a sliding window and first tokens that stay
+// visible (sinks): the forward.
+//
+// Query q of a sequence sees the keys k <= q with k > q - window or k < sinks:
+//   O_q = sum_k softmax_k(scale q.k) v_k,   LSE_q = ln sum_k exp(scale q.k).
+// H query heads share Hkv key/value heads (G = H / Hkv each).
+//
+// The work is 4 d flops a visible pair against 4 d bytes a row, so it is bound
+// by the tensor cores (and, next to them, by the exponentials: 128 x 128 of a
+// tile take 1024 cycles of the SM's 16 a clock, as long as its two products).
+//
+// One persistent CTA per SM walks items.  An item is two tiles of 128 queries
+// ("slots") that see the same keys: the same rows of two heads of a group, or
+// two neighbouring tiles of a head where G is odd.  They share every key and
+// value tile that TMA brings in, which halves the shared-memory fill and lets
+// the tensor core work for one slot while the other's softmax runs:
+//   warps 0-3, 4-7   softmax of slot 0, 1: one thread per query row
+//   warps 8-11       epilogue of both slots, beside the next item's first steps
+//   warp 12          tcgen05.mma issuer (one thread)
+//   warp 13          TMA producer
+// S = Q K^T lands in TMEM (128 columns a slot); the softmax writes P over it as
+// bf16 and O += P V takes P from there.  A slot's next S is issued behind its
+// P V, so the order of issue protects P.  TMEM: 2 x 128 columns of S, 2 x d of O.
+//
+// The walk is the sink tiles, then the window's tiles.  Only tiles that cross the
+// diagonal, the window's lower edge or the sequence's end pay for masks, and a
+// sink tile of up to 32 visible keys is taken with 32 columns instead of 128.
+//
+// Softmax: maxima on raw scores, lazy rescale of O (only when the maximum grows by
+// more than 2^8, so P <= 2^8), 2^x with the scale folded in, part of it by a
+// polynomial on the FMA pipe.  P is rounded to bf16 (2^-9 relative, like the
+// operands it meets); maxima, sums and O are fp32.
+//
+// Every wait is bounded.
+#include "bsa_window.cuh"
+
+namespace bsa {
+namespace wfwd {
+
+using namespace bsa::win;
+
+constexpr int kSlots = 2;
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr float kRescale = 8.f;  // log2 units
+
+__device__ unsigned int g_wfwd_status;
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE = kTile * D * 2;
+  static constexpr int ATOMS = D / 64;
+  static constexpr int STAGES = D == 128 ? 5 : 8;     // tiles of K or V in flight
+  static constexpr int TMEM_O = 256;                  // slot s: S at 128 s, O at 256 + s D
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int OFF_KV = kSlots * TILE;
+  static constexpr int OFF_CTL = OFF_KV + STAGES * TILE;
+};
+
+struct Ctl {
+  uint64_t q_full[kSlots], q_empty[kSlots];
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[kSlots], p_full[kSlots];
+  uint64_t o_full[kSlots], o_free[kSlots];
+  uint64_t ml_full[kSlots], ml_free[kSlots];
+  uint64_t fix, final_bar;
+  uint32_t tmem_base;
+  volatile int abort;
+  float2 ml[kSlots][kTile];  // (maximum in log2 units, sum) of each row
+};
+
+struct Args {
+  const int32_t* lens;
+  __nv_bfloat16* O;
+  long long o_sb, o_sh, o_sn;
+  float* LSE;
+  int B, H, Hkv, G, N;
+  int pairs;          // items per tile row of a cached head (G even: G / 2; else G)
+  int rows;           // tile rows: q tiles (G even) or pairs of them
+  int by_head;        // the two slots are two heads
+  int window, sinks;
+  long long items;
+  float scale_log2;
+};
+
+struct Item {
+  int b, hk, len;
+  int h[kSlots], q0[kSlots];
+  int sink_steps, first, steps;
+  __device__ __forceinline__ int key0(int j) const {
+    return (j < sink_steps ? j : first + j - sink_steps) * kTile;
+  }
+};
+
+__device__ __forceinline__ Item item_of(const Args& a, long long i) {
+  Item it;
+  const int p = static_cast<int>(i % a.pairs);
+  long long r = i / a.pairs;
+  const int row = static_cast<int>(r % a.rows);
+  r /= a.rows;
+  it.hk = static_cast<int>(r % a.Hkv);
+  it.b = static_cast<int>(r / a.Hkv);
+  if (a.by_head) {
+    it.h[0] = it.hk * a.G + 2 * p;
+    it.h[1] = it.h[0] + 1;
+    it.q0[0] = it.q0[1] = row * kTile;
+  } else {
+    it.h[0] = it.h[1] = it.hk * a.G + p;
+    it.q0[0] = row * 2 * kTile;
+    it.q0[1] = it.q0[0] + kTile;
+  }
+  it.len = length_of(a.lens, it.b, a.N, &g_wfwd_status);
+  const int top = min(it.q0[1] + kTile, it.len) - 1;  // last query with keys
+  const int lo = max(0, it.q0[0] - a.window + 1);
+  it.first = lo / kTile;
+  it.sink_steps = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
+  it.steps = it.q0[0] < it.len ? it.sink_steps + top / kTile - it.first + 1 : 0;
+  return it;
+}
+
+// Columns a step takes: 32 where a sink tile outside the window shows no more.
+__device__ __forceinline__ bool narrow_step(const Args& a, const Item& it, int j) {
+  return j < it.sink_steps && a.sinks - j * kTile <= 32;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl) {
+  const bool ok = wait_bounded(bar, parity, &ctl->abort, &g_wfwd_status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// ------------------------------------------------------------------ producer
+template <int D>
+__device__ void load_role(const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
+                          const Args& a, unsigned char* smem, Ctl* ctl) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t n = 0, items = 0, fixes = 0;
+  bool ok = true;
+  for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+    const Item it = item_of(a, i);
+    if (it.steps == 0) continue;
+    for (int s = 0; s < kSlots && ok; ++s) {
+      if (items > 0) ok = warp_wait(&ctl->q_empty[s], (items - 1) & 1, ctl);
+      if (ok && lane == 0) {
+        mbar_arrive_expect_tx(&ctl->q_full[s], C::TILE);
+        for (int c = 0; c < C::ATOMS; ++c)
+          tma_load_4d(smem + s * C::TILE + c * kAtom, mq, &ctl->q_full[s], 64 * c, it.q0[s], it.h[s], it.b);
+      }
+    }
+    ++items;
+    for (int j = 0; j < it.steps && ok; ++j) {
+      const int k0 = it.key0(j);
+      for (int w = 0; w < 2 && ok; ++w) {
+        const int st = n % C::STAGES;
+        if (n >= C::STAGES) ok = warp_wait(&ctl->kv_empty[st], (n / C::STAGES - 1) & 1, ctl);
+        if (!ok) break;
+        unsigned char* dst = smem + C::OFF_KV + st * C::TILE;
+        // Rows past the sequence's end may hold anything; their weight is 0, but
+        // 0 times a NaN is not: they are cleared before the value tile is used.
+        const bool fix = w == 1 && k0 + kTile > it.len && it.len < a.N;
+        uint64_t* bar = fix ? &ctl->fix : &ctl->kv_full[st];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, C::TILE);
+          for (int c = 0; c < C::ATOMS; ++c)
+            tma_load_4d(dst + c * kAtom, w == 0 ? mk : mv, bar, 64 * c, k0, it.hk, it.b);
+        }
+        if (fix) {
+          ok = warp_wait(&ctl->fix, fixes & 1, ctl);
+          ++fixes;
+          if (ok) {
+            for (int e = lane; e < (k0 + kTile - it.len) * 8 * C::ATOMS; e += 32) {
+              const int r = it.len - k0 + e / (8 * C::ATOMS), c = e % (8 * C::ATOMS);
+              *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
+        }
+        ++n;
+      }
+    }
+  }
+  // Copies in flight must land before the block's shared memory goes away.
+  if (lane == 0) {
+    for (int s = 0; s < kSlots; ++s)
+      if (items > 0) wait_drain(&ctl->q_full[s], (items - 1) & 1, &g_wfwd_status);
+    for (uint32_t st = 0; st < static_cast<uint32_t>(C::STAGES); ++st)
+      if (n > st) wait_drain(&ctl->kv_full[st], ((n - 1 - st) / C::STAGES) & 1, &g_wfwd_status);
+    if (fixes > 0) wait_drain(&ctl->fix, (fixes - 1) & 1, &g_wfwd_status);
+  }
+}
+
+// ---------------------------------------------------------------- MMA issuer
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tmem, uint32_t sbase, int s, int st, bool narrow) {
+  using C = Cfg<D>;
+  const uint64_t ad = sdesc_sw128(sbase + s * C::TILE, 16, 1024);
+  const uint64_t bd = sdesc_sw128(sbase + C::OFF_KV + st * C::TILE, 16, 1024);
+  const uint32_t idesc = narrow ? idesc_bf16_f32(128, 32, false, false) : idesc_bf16_f32(128, 128, false, false);
+  umma_qk_chain<D / 16>(tmem + s * 128, static_cast<uint32_t>(ad), static_cast<uint32_t>(ad >> 32),
+                        static_cast<uint32_t>(bd), static_cast<uint32_t>(bd >> 32), idesc);
+}
+
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sbase, int s, int st, bool narrow, bool add) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
+  const uint64_t bd = sdesc_sw128(sbase + C::OFF_KV + st * C::TILE, kAtom, 1024);
+  if (narrow) {
+    for (int kk = 0; kk < 2; ++kk)
+      umma_bf16_ts(tmem + C::TMEM_O + s * D, tmem + s * 128 + 8 * kk, bd + ((kk * 16 * 128) >> 4), kIdesc,
+                   (add || kk > 0) ? 1u : 0u);
+  } else {
+    umma_pv_chain8(tmem + C::TMEM_O + s * D, tmem + s * 128, static_cast<uint32_t>(bd),
+                   static_cast<uint32_t>(bd >> 32), kIdesc, add ? 1u : 0u);
+  }
+}
+
+template <int D>
+__device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t tmem) {
+  using C = Cfg<D>;
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t n = 0, items = 0, p_seen = 0;  // tiles consumed, items begun, steps per slot
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return wait_bounded(bar, parity, &ctl->abort, &g_wfwd_status);
+  };
+  bool ok = true;
+  for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+    const Item it = item_of(a, i);
+    if (it.steps == 0) continue;
+    int kst = n % C::STAGES;
+    ok = wait(&ctl->kv_full[kst], (n / C::STAGES) & 1);
+    for (int s = 0; s < kSlots && ok; ++s) {
+      ok = wait(&ctl->q_full[s], items & 1);
+      if (!ok) break;
+      tc_fence_after();
+      issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, 0));
+      umma_commit(&ctl->s_full[s]);
+      if (it.steps == 1) umma_commit(&ctl->q_empty[s]);
+    }
+    if (!ok) break;
+    umma_commit(&ctl->kv_empty[kst]);
+    ++n;
+    for (int j = 0; j < it.steps && ok; ++j) {
+      const int vst = n % C::STAGES;
+      const uint32_t vpar = (n / C::STAGES) & 1;
+      ++n;
+      const bool more = j + 1 < it.steps;
+      kst = n % C::STAGES;
+      const uint32_t kpar = (n / C::STAGES) & 1;
+      if (more) ++n;
+      for (int s = 0; s < kSlots; ++s) {
+        if (s == 0) ok = wait(&ctl->kv_full[vst], vpar);
+        if (j == 0 && items > 0) ok = ok && wait(&ctl->o_free[s], (items - 1) & 1);
+        ok = ok && wait(&ctl->p_full[s], p_seen & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv<D>(tmem, sbase, s, vst, narrow_step(a, it, j), j > 0);
+        if (!more) umma_commit(&ctl->o_full[s]);
+        if (s == 1) umma_commit(&ctl->kv_empty[vst]);
+        if (more) {
+          if (s == 0) {
+            ok = wait(&ctl->kv_full[kst], kpar);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, j + 1));
+          umma_commit(&ctl->s_full[s]);
+          if (j + 2 == it.steps) umma_commit(&ctl->q_empty[s]);
+          if (s == 1) umma_commit(&ctl->kv_empty[kst]);
+        }
+      }
+      ++p_seen;
+    }
+    ++items;
+  }
+  // Every MMA issued must complete before TMEM is released.
+  umma_commit(&ctl->final_bar);
+  wait_drain(&ctl->final_bar, 0, &g_wfwd_status);
+}
+
+// ------------------------------------------------------------------- softmax
+// One step of one query row: NC scores to NC / 2 columns of P.
+template <int D, int NC>
+__device__ __forceinline__ void softmax_step(uint32_t t_s, uint32_t t_o, float sl2, bool neg, bool masked,
+                                             int c_hi, int c_lo, int c_sink, bool have_o, float& m, float& l) {
+  constexpr float kNegInf = -INFINITY;
+  float x[NC];
+  if constexpr (NC == 128)
+    tmem_ld128_wait(t_s, x);
+  else
+    tmem_ld32f_wait(t_s, x);
+  if (neg) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) x[c] = -x[c];
+  }
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (c > c_hi || (c < c_lo && c >= c_sink)) x[c] = kNegInf;
+  }
+  float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+#pragma unroll
+  for (int c = 0; c < NC; c += 8) {
+    m0 = max3f(m0, x[c], x[c + 1]);
+    m1 = max3f(m1, x[c + 2], x[c + 3]);
+    m2 = max3f(m2, x[c + 4], x[c + 5]);
+    m3 = max3f(m3, x[c + 6], x[c + 7]);
+  }
+  const float hm = max3f(fmaxf(m0, m1), m2, m3) * sl2;
+  const bool need = hm > m + kRescale;
+  if (__any_sync(0xffffffffu, need)) {
+    float f = 1.f;
+    if (need) {
+      f = m == kNegInf ? 1.f : ex2_approx(m - hm);
+      m = hm;
+    }
+    l *= f;
+    // this step's S is ready, so the P V of every step before has completed
+    if (have_o && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t w[32];
+        tmem_ld32_wait(t_o + c0, w);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+        tmem_st32_wait(t_o + c0, w);
+      }
+    }
+  }
+  const float nm = m == kNegInf ? 0.f : -m;
+  float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
+#pragma unroll
+  for (int g = 0; g < NC; g += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      float p0 = x[g + c], p1 = x[g + c + 1], p2 = x[g + c + 2], p3 = x[g + c + 3];
+      fma2(p0, p1, sl2, nm);
+      fma2(p2, p3, sl2, nm);
+      if (D == 128 && (c / 4) % 4 == 3) {  // this share of 2^x on the FMA pipe
+        exp2_poly2(p0, p1);
+        exp2_poly2(p2, p3);
+      } else {
+        p0 = ex2_approx(p0);
+        p1 = ex2_approx(p1);
+        p2 = ex2_approx(p2);
+        p3 = ex2_approx(p3);
+      }
+      acc2(sa, sb, p0, p1);
+      acc2(sc, sd, p2, p3);
+      pk[c / 2] = pack_bf16x2(p0, p1);
+      pk[c / 2 + 1] = pack_bf16x2(p2, p3);
+    }
+    tmem_st16(t_s + g / 2, pk);
+  }
+  l += (sa + sb) + (sc + sd);
+}
+
+template <int D>
+__device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
+  using C = Cfg<D>;
+  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = wq * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  const uint32_t t_s = t_lane + s * 128, t_o = t_lane + C::TMEM_O + s * D;
+  const bool neg = a.scale_log2 < 0.f;
+  const float sl2 = fabsf(a.scale_log2);
+  uint32_t seen = 0, items = 0;
+  for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+    const Item it = item_of(a, i);
+    if (it.steps == 0) continue;
+    const int q = it.q0[s] + row;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < it.steps; ++j) {
+      const int k0 = it.key0(j);
+      // all keys of the tile are visible to all of its rows
+      const bool full = k0 + kTile - 1 <= it.q0[s] &&
+                        (k0 > it.q0[s] + kTile - 1 - a.window || k0 + kTile <= a.sinks);
+      if (!warp_wait(&ctl->s_full[s], seen & 1, ctl)) return;
+      ++seen;
+      tc_fence_after();
+      if (narrow_step(a, it, j))
+        softmax_step<D, 32>(t_s, t_o, sl2, neg, true, q - k0, q - a.window + 1 - k0, a.sinks - k0, j > 0, m, l);
+      else
+        softmax_step<D, 128>(t_s, t_o, sl2, neg, !full, q - k0, q - a.window + 1 - k0, a.sinks - k0, j > 0, m, l);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full[s]);
+    }
+    if (items > 0 && !warp_wait(&ctl->ml_free[s], (items - 1) & 1, ctl)) return;
+    ctl->ml[s][row] = make_float2(m, l);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->ml_full[s]);
+    ++items;
+  }
+}
+
+// ------------------------------------------------------------------ epilogue
+template <int D>
+__device__ void epilogue_role(const Args& a, Ctl* ctl, uint32_t tmem) {
+  using C = Cfg<D>;
+  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = wq * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  uint32_t items = 0;
+  for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+    const Item it = item_of(a, i);
+    for (int s = 0; s < kSlots; ++s) {
+      const int q = it.q0[s] + row;
+      float m = -INFINITY, l = 0.f;
+      if (it.steps > 0) {
+        if (!warp_wait(&ctl->ml_full[s], items & 1, ctl)) return;
+        const float2 ml = ctl->ml[s][row];
+        m = ml.x;
+        l = ml.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->ml_free[s]);
+        if (!warp_wait(&ctl->o_full[s], items & 1, ctl)) return;
+        tc_fence_after();
+      }
+      const bool live = q < it.len;
+      const float inv = 1.f / l;
+      uint4* out = reinterpret_cast<uint4*>(a.O + it.b * a.o_sb + it.h[s] * a.o_sh + static_cast<long long>(q) * a.o_sn);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t w[32];
+        if (it.steps > 0) tmem_ld32_wait(t_lane + C::TMEM_O + s * D + c0, w);
+        if (q < a.N) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 r = make_uint4(0u, 0u, 0u, 0u);
+            if (live) {
+              r.x = pack_bf16x2(__uint_as_float(w[8 * v]) * inv, __uint_as_float(w[8 * v + 1]) * inv);
+              r.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * inv, __uint_as_float(w[8 * v + 3]) * inv);
+              r.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * inv, __uint_as_float(w[8 * v + 5]) * inv);
+              r.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * inv, __uint_as_float(w[8 * v + 7]) * inv);
+            }
+            out[c0 / 8 + v] = r;
+          }
+        }
+      }
+      if (it.steps > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_free[s]);
+      }
+      if (q < a.N)
+        a.LSE[(static_cast<long long>(it.b) * a.H + it.h[s]) * a.N + q] =
+            live ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+    if (it.steps > 0) ++items;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                          const __grid_constant__ CUtensorMap mv, const Args a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];  // swizzle atoms need 1024 bytes
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_wfwd_status, BSA_STATUS_INTERNAL);
+    return;
+  }
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_empty[s], 1);
+      mbar_init(&ctl->s_full[s], 1);
+      mbar_init(&ctl->p_full[s], 4);
+      mbar_init(&ctl->o_full[s], 1);
+      mbar_init(&ctl->o_free[s], 4);
+      mbar_init(&ctl->ml_full[s], 4);
+      mbar_init(&ctl->ml_free[s], 4);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&ctl->kv_full[i], 1);
+      mbar_init(&ctl->kv_empty[i], 1);
+    }
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->final_bar, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  // 512 threads are launched with 128 registers: 256 x 192 + 128 x 80 + 128 x 48
+  if (warp < 8) {
+    regs_more<192>();
+    softmax_role<D>(warp >> 2, a, ctl, tmem);
+    __syncwarp();
+  } else if (warp < 12) {
+    regs_less<80>();
+    epilogue_role<D>(a, ctl, tmem);
+    __syncwarp();
+  } else {
+    regs_less<48>();
+    if (warp == kMmaWarp) {
+      if ((threadIdx.x & 31) == 0) mma_role<D>(a, smem, ctl, tmem);
+    } else if (warp == kLoadWarp) {
+      load_role<D>(&mq, &mk, &mv, a, smem, ctl);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const Args& a, cudaStream_t s) {
+  using C = Cfg<D>;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, q, a.B, a.H, a.N, D) || !make_map(&mk, k, a.B, a.Hkv, a.N, D) ||
+      !make_map(&mv, v, a.B, a.Hkv, a.N, D))
+    return BSA_ERR_CUDA;
+  const int smem = C::OFF_CTL + static_cast<int>(sizeof(Ctl));
+  static_assert(C::OFF_CTL + sizeof(Ctl) <= 232448, "227 KB of shared memory");
+  const auto kernel = window_forward_kernel<D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  const long long sms = sm_count();
+  kernel<<<static_cast<unsigned>(a.items < sms ? a.items : sms), kThreads, smem, s>>>(mq, mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace wfwd
+
+int take_status(const void* symbol, uint32_t* status, int clear);
+int window_forward_status(uint32_t* status, int clear) {
+  return take_status(&wfwd::g_wfwd_status, status, clear);
+}
+}  // namespace bsa
+
+extern "C" int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v,
+                                  const int32_t* lens, int B, int H, int Hkv, int N, int d, int window,
+                                  int sinks, float scale, const bsa_view* o, float* LSE, void* stream) {
+  using namespace bsa::wfwd;
+  if (B < 1 || H < 1 || Hkv < 1 || N < 1 || d < 1 || H % Hkv != 0 || window < 1 || sinks < 0 ||
+      !std::isfinite(scale) || !LSE || (reinterpret_cast<uintptr_t>(LSE) & 3u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  if (!view_ok(q, B, H, N, d) || !view_ok(k, B, Hkv, N, d) || !view_ok(v, B, Hkv, N, d) || !view_ok(o, B, H, N, d))
+    return BSA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  if (N > (1 << 30)) return BSA_ERR_UNSUPPORTED;
+  Args a = {};
+  a.lens = lens;
+  a.O = static_cast<__nv_bfloat16*>(const_cast<void*>(o->data));
+  a.o_sb = B > 1 ? o->stride_b : 0;
+  a.o_sh = H > 1 ? o->stride_h : 0;
+  a.o_sn = N > 1 ? o->stride_n : 0;
+  a.LSE = LSE;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.N = N;
+  const int tiles = (N + kTile - 1) / kTile;
+  a.by_head = a.G % 2 == 0;
+  a.pairs = a.by_head ? a.G / 2 : a.G;
+  a.rows = a.by_head ? tiles : (tiles + 1) / 2;
+  a.window = window < N ? window : N;
+  a.sinks = sinks < N ? sinks : N;
+  a.items = static_cast<long long>(B) * Hkv * a.rows * a.pairs;
+  // never 0: hidden scores are -inf times it, and must stay -inf
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch<64>(q, k, v, a, s) : launch<128>(q, k, v, a, s);
+}

@@ -35,6 +35,7 @@ def _declare(lib) -> None:
             ("bsa_q4_decode", [_vp, _vp, _vp, cache, _vp, _vp, _vp, i, i, f, _vp, _vp, _vp]),
             ("bsa_q4_window_decode", [_vp, _vp, _vp, cache, _vp, i, i, i, f, _vp, _vp, _vp]),
             ("bsa_window_decode", [_vp] * 6 + [i] * 7 + [f, _vp, _vp, _vp]),
+            ("bsa_window_forward", [view] * 3 + [_vp] + [i] * 7 + [f, view, _vp, _vp]),
             ("bsa_stream_status", [ctypes.POINTER(ctypes.c_uint32), i])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, types
@@ -237,6 +238,41 @@ def window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int = 0, sca
     qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
     _call(device, "bsa_window_decode", qp, kn, vn, kc, vc, _ints("seq_len", seq_len, B, device), B, H, Hkv, L, d,
           int(window), int(sinks), scale, out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def _heads(q, k):
+    """(B, H, Hkv, N, d) of [B, H, N, d] queries and [B, Hkv, N, d] keys."""
+    if q.dim() != 4 or k.dim() != 4 or q.shape[1] % max(int(k.shape[1]), 1):
+        raise ValueError("q must be [B, H, N, d] and k, v [B, Hkv, N, d], H a multiple of Hkv")
+    B, H, N, d = q.shape
+    return int(B), int(H), int(k.shape[1]), int(N), int(d)
+
+
+def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] = None, lens=None, out=None,
+                   lse=None):
+    """Attention with a sliding window and first tokens that stay visible
+    (bsa_window_forward): query i sees the keys k <= i with k > i - window or k < sinks.
+
+    q: CUDA bf16 [B, H, N, d]; k, v: [B, Hkv, N, d]; any strides that are
+    multiples of 8 with d contiguous and rows that do not overlap, so a
+    sequence-major tensor is passed as its transpose(1, 2).  lens: CUDA int32
+    [B], tokens of each sequence (all N where None); rows past them give O = 0
+    and LSE = -inf.  Returns (O like q, LSE fp32 [B, H, N]).
+    """
+    import torch
+
+    B, H, Hkv, N, d = _heads(q, k)
+    device = q.device
+    qv = _view("q", q, (B, H, N, d), device)
+    kv, vv = _view("k", k, (B, Hkv, N, d), device), _view("v", v, (B, Hkv, N, d), device)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
+    _call(device, "bsa_window_forward", qv, kv, vv, None if lens is None else _ints("lens", lens, B, device), B, H,
+          Hkv, N, d, int(window), int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+          _view("out", out, (B, H, N, d), device), _rows("lse", lse, (B, H, N), device, torch.float32))
     return out, lse
 
 

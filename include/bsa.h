@@ -454,6 +454,27 @@ int bsa_window_decode(const void* q, const void* k_new, const void* v_new, void*
                       const int32_t* seq_len, int B, int H, int Hkv, int L, int d, int window, int sinks,
                       float scale, void* O, float* LSE, void* stream);
 
+/*
+ * bsa_window_forward -- attention with a sliding window and first tokens that
+ * stay visible: query i of a sequence sees the keys k <= i with k > i - window
+ * or k < sinks;
+ *   O[b,h,i] = sum softmax(scale q.k) v,   LSE[b,h,i] = ln sum exp(scale q.k).
+ * q, o: [B, H, N, d] views; k, v: [B, Hkv, N, d] views (bf16, device; query head
+ * h reads key/value head h / (H / Hkv)); LSE: device fp32 [B, H, N] contiguous.
+ * lens: device int32 [B], tokens of each sequence (0..N), or NULL: N each.  Rows
+ * from lens[b] on may hold anything; their O is 0 and their LSE -inf.  A bad
+ * length sets BSA_STATUS_BAD_SEQ_LEN and counts as 0.  A NaN or infinity in a key
+ * or value row can reach every query of the same and the next 128-query tile,
+ * also those that do not see the row.
+ * Strides (of dimensions of more than one entry): positive multiples of 8, at
+ * least d, below 2^39.  Any N up to 2^30, any H / Hkv; d in {64, 128}.  One
+ * launch, enqueued on `stream`; nothing allocated or synchronised; the same bits
+ * every run.
+ */
+int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v, const int32_t* lens, int B,
+                       int H, int Hkv, int N, int d, int window, int sinks, float scale, const bsa_view* o,
+                       float* LSE, void* stream);
+
 /* bsa_stream_status -- as bsa_device_status, for the status words of the
  * functions of this section. */
 int bsa_stream_status(uint32_t* status, int clear);
