@@ -448,4 +448,5 @@ def version() -> int:
 
 from . import long_stream  # noqa: E402
 from .long_stream import (Q4Cache, q4_cache, q4_decode, q4_read, q4_window_decode,  # noqa: E402,F401
-                          q4_write, stream_status, window_decode, window_forward)
+                          q4_write, stream_status, window_backward,
+                          window_backward_workspace_bytes, window_decode, window_forward)

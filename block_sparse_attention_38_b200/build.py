@@ -7,7 +7,7 @@ translation units: the forward launcher with its kernel (bsa_forward.cu),
 top-k block selection (bsa_topk.cu), the decode step (bsa_decode.cu), the
 backward pass (bsa_backward.cu), the 4-bit cache (bsa_q4_cache.cu) and the
 decode steps over long caches (bsa_stream_decode.cu) and sliding-window
-attention (bsa_window_fwd.cu).  CUDA runtime is linked
+attention (bsa_window_fwd.cu, bsa_window_bwd.cu).  CUDA runtime is linked
 statically; the driver's tensor-map encoder is looked up at run time, so the
 library loads on a machine without a GPU (only compute calls need one).
 """
@@ -24,7 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "bsa_pattern.cpp"), os.path.join(CSRC, "bsa_forward.cu"),
            os.path.join(CSRC, "bsa_topk.cu"), os.path.join(CSRC, "bsa_decode.cu"),
            os.path.join(CSRC, "bsa_backward.cu"), os.path.join(CSRC, "bsa_q4_cache.cu"),
-           os.path.join(CSRC, "bsa_stream_decode.cu"), os.path.join(CSRC, "bsa_window_fwd.cu")]
+           os.path.join(CSRC, "bsa_stream_decode.cu"), os.path.join(CSRC, "bsa_window_fwd.cu"),
+           os.path.join(CSRC, "bsa_window_bwd.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "bsa.h")]
 LIB = os.path.join(HERE, "libbsa.so")

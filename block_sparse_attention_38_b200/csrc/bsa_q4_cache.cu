@@ -269,6 +269,7 @@ int take_status(const void* symbol, uint32_t* status, int clear) {
 int q4_status(uint32_t* status, int clear) { return take_status(&q4::g_q4_status, status, clear); }
 int stream_decode_status(uint32_t* status, int clear);
 int window_forward_status(uint32_t* status, int clear);
+int window_backward_status(uint32_t* status, int clear);
 }  // namespace bsa
 
 extern "C" int bsa_stream_status(uint32_t* status, int clear) {
@@ -278,6 +279,7 @@ extern "C" int bsa_stream_status(uint32_t* status, int clear) {
   int rc = bsa::q4_status(&v, clear);
   if (rc == BSA_OK) rc = bsa::stream_decode_status(&v, clear);
   if (rc == BSA_OK) rc = bsa::window_forward_status(&v, clear);
+  if (rc == BSA_OK) rc = bsa::window_backward_status(&v, clear);
   if (rc == BSA_OK) *status = v;
   return rc;
 }

@@ -1,0 +1,974 @@
+// bsa_window_bwd.cu -- attention with a sliding window and first tokens that stay
+// visible (sinks): the gradients of bsa_window_fwd.cu's forward.
+//
+// With P_qk = exp(scale q.k - LSE_q) over the visible pairs and D_q = dO_q . O_q:
+//   dV_k = sum_q P dO_q,  dS = P (dO_q . v_k - D_q),
+//   dQ_q = scale sum_k dS k_k,  dK_k = scale sum_q dS q_q,
+// the sums for dK and dV over the G query heads that share the key/value head too.
+//
+// 10 d flops a visible pair, bound by the tensor cores.  Two tile kernels, each
+// output row produced by one CTA (no atomics, the same bits every run), at the
+// price of computing S and dP twice (14 d flops issued):
+//   dkdv  one CTA per 128-key tile; a step is one query tile of one head:
+//           S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
+//   dq    persistent CTAs over (head, 128-query tile); a step is one key tile:
+//           S = Q K^T, dP = dO V^T;  dQ += dS K
+// P and dS go to the second products from TMEM as bf16 (2^-8 at most, like the
+// operands they meet); scores, P before that rounding and sums are fp32.
+//
+// In both, eight warps (one thread per half row) turn S into P (phase A), then dP
+// into dS (phase B), while the tensor core works on the products of the other
+// phase: dkdv issues dP(j) | dV(j), S(j+1) | dK(j), dP(j+1) | ..., so that A(j+1)
+// runs beside dK(j) and dP(j+1), and B(j) beside dV(j) and S(j+1).  The order of
+// issue by the one MMA thread protects P and dS, which lie over S and dP.
+// TMEM, 512 columns at d = 128: S, dP, dV, dK; and S, dP, two dQ (the next tile
+// begins while the last one's dQ is stored).
+//
+// The keys of the sink tiles are seen by every later query.  Their far queries
+// (beyond the window) are cut into chunks that run as CTAs of their own and leave
+// fp32 partial sums in the workspace, added up in a fixed order by sink_kernel.
+//
+// Every wait is bounded.
+#include "bsa_window.cuh"
+
+namespace bsa {
+namespace wbwd {
+
+using namespace bsa::win;
+
+constexpr int kThreads = 384;            // 8 elementwise warps, MMA, producer, 2 idle
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMaxChunks = 32;
+
+__device__ unsigned int g_wbwd_status;
+
+struct Args {
+  const int32_t* lens;
+  const float* LSE;          // [B, H, N]
+  const float* Dq;           // [B, H, N]
+  __nv_bfloat16* out[2];     // dV, dK, or dQ
+  long long sb[2], sh[2], sn[2];
+  float* part;               // [B * Hkv, sink tiles, 1 + chunks, 2, 128, d]
+  int B, H, Hkv, G, N, tiles;
+  int window, sinks;
+  int sink_tiles;            // key tiles with sinks that have far queries
+  int chunks, chunk_tiles;   // far chunks per sink tile, query tiles in each
+  long long items;
+  float scale, scale_log2;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE = kTile * D * 2;
+  static constexpr int ATOMS = D / 64;
+};
+
+// Clears rows from `from` on of a tile that TMA has written, by one warp: what
+// lies past a sequence's end may be NaN, and its weight 0 does not remove that.
+template <int D>
+__device__ __forceinline__ void clear_rows(unsigned char* tile, int from, int lane) {
+  constexpr int P = D / 8;
+  for (int e = lane; e < (kTile - from) * P; e += 32) {
+    const int r = from + e / P, c = e % P;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_shared();
+}
+
+// D (+)= A B^T over the d channels, both tiles K-major in shared memory; n columns.
+template <int D>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
+  const uint64_t ad = sdesc_sw128(a_smem, 16, 1024), bd = sdesc_sw128(b_smem, 16, 1024);
+  umma_qk_chain<D / 16>(d_tmem, static_cast<uint32_t>(ad), static_cast<uint32_t>(ad >> 32),
+                        static_cast<uint32_t>(bd), static_cast<uint32_t>(bd >> 32), idesc);
+}
+
+// C (+)= A B with A in TMEM (bf16 pairs; columns 64 h .. 64 h + 31 hold entries
+// 64 h .. 64 h + 63 of the summed index) and B a tile read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_ts(uint32_t c_tmem, uint32_t a_tmem, uint32_t b_smem, int slices, bool add) {
+  constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
+  const uint64_t bd = sdesc_sw128(b_smem, kAtom, 1024);
+#pragma unroll 8
+  for (int kk = 0; kk < slices; ++kk)
+    umma_bf16_ts(c_tmem, a_tmem + (kk >> 2) * 64 + (kk & 3) * 8, bd + ((kk * 16 * 128) >> 4), kIdesc,
+                 (add || kk > 0) ? 1u : 0u);
+}
+
+// 2^x of 32 scaled scores: every fourth group of four on the FMA pipe.
+__device__ __forceinline__ void exp2_four(float& a, float& b, float& c, float& d, bool poly) {
+  if (poly) {
+    exp2_poly2(a, b);
+    exp2_poly2(c, d);
+  } else {
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    c = ex2_approx(c);
+    d = ex2_approx(d);
+  }
+}
+
+// 32 accumulator columns of this thread's row, times mul, to 32 bf16.
+__device__ __forceinline__ void store_row32(uint32_t taddr, float mul, bool zero, uint4* dst, bool write) {
+  uint32_t w[32];
+  tmem_ld32_wait(taddr, w);
+  if (!write) return;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (!zero) {
+      r.x = pack_bf16x2(__uint_as_float(w[8 * v]) * mul, __uint_as_float(w[8 * v + 1]) * mul);
+      r.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * mul, __uint_as_float(w[8 * v + 3]) * mul);
+      r.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * mul, __uint_as_float(w[8 * v + 5]) * mul);
+      r.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * mul, __uint_as_float(w[8 * v + 7]) * mul);
+    }
+    dst[v] = r;
+  }
+}
+
+// ------------------------------------------------------------ D = dO . O
+struct DotArgs {
+  const __nv_bfloat16 *o, *g;
+  long long osb, osh, osn, gsb, gsh, gsn;
+  float* D;
+  long long rows;
+  int H, N;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) dot_kernel(const DotArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, part = lane % LPR;
+  const long long r = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * RPW + lane / LPR;
+  float acc = 0.f;
+  if (r < a.rows) {
+    const long long bh = r / a.N;
+    const long long q = r - bh * a.N, b = bh / a.H, h = bh - b * a.H;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + b * a.osb + h * a.osh + q * a.osn + 8 * part));
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(a.g + b * a.gsb + h * a.gsh + q * a.gsn + 8 * part));
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), acc);
+      acc = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), acc);
+    }
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (r < a.rows && part == 0) a.D[r] = acc;
+}
+
+// ------------------------------------------------------------------- dK, dV
+struct KvCtl {
+  uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2];
+  uint64_t s_full, p_ready, dp_full, ds_ready, acc_full, fix;
+  uint32_t tmem_base;
+  volatile int abort;
+  alignas(16) float lse2[2][kTile];  // of a stage's queries: LSE log2(e), and D
+  alignas(16) float dq[2][kTile];
+};
+
+struct KvItem {
+  int b, hk, kt, k0, len, slot;      // slot: the partial result's place, or -1
+  int first, count;                  // query tiles
+};
+
+__device__ __forceinline__ KvItem kv_item(const Args& a, long long i) {
+  KvItem it;
+  const long long main_items = static_cast<long long>(a.B) * a.Hkv * a.tiles;
+  long long bh;
+  int chunk = -1;
+  if (i < main_items) {
+    it.kt = static_cast<int>(i % a.tiles);
+    bh = i / a.tiles;
+  } else {
+    i -= main_items;
+    chunk = static_cast<int>(i % a.chunks);
+    i /= a.chunks;
+    it.kt = static_cast<int>(i % a.sink_tiles);
+    bh = i / a.sink_tiles;
+  }
+  it.b = static_cast<int>(bh / a.Hkv);
+  it.hk = static_cast<int>(bh % a.Hkv);
+  it.k0 = it.kt * kTile;
+  it.len = length_of(a.lens, it.b, a.N, &g_wbwd_status);
+  const int last = (it.len - 1) / kTile;                       // last query tile with queries
+  const int near = static_cast<int>(min(static_cast<long long>(a.tiles) - 1,
+                                        (static_cast<long long>(it.k0) + kTile - 1 + a.window - 1) / kTile));
+  int end;
+  if (chunk < 0) {
+    it.first = it.kt;
+    end = min(near, last);
+    it.slot = it.kt < a.sink_tiles ? 0 : -1;
+  } else {
+    it.first = near + 1 + chunk * a.chunk_tiles;
+    end = min(it.first + a.chunk_tiles - 1, last);
+    it.slot = 1 + chunk;
+  }
+  it.count = it.k0 < it.len ? max(0, end - it.first + 1) : 0;
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args a) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdesc = idesc_bf16_f32(128, 128, false, false);
+  constexpr int T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_wbwd_status, BSA_STATUS_INTERNAL);
+    return;
+  }
+  unsigned char *sK = smem, *sV = smem + C::TILE, *sQ = smem + 2 * C::TILE, *sO = smem + 4 * C::TILE;
+  KvCtl* ctl = reinterpret_cast<KvCtl*>(smem + 6 * C::TILE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const KvItem it = kv_item(a, blockIdx.x);
+  const int steps = it.count * a.G;
+
+  if (tid == 0) {
+    mbar_init(&ctl->kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_empty[s], 1);
+      mbar_init(&ctl->do_full[s], 1);
+      mbar_init(&ctl->do_empty[s], 1);
+    }
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->p_ready, 8);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->ds_ready, 8);
+    mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->fix, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return wait_bounded(bar, parity, &ctl->abort, &g_wbwd_status);
+  };
+
+  if (warp == kLoadWarp && steps > 0) {
+    // ------------------------------------------------------------- producer
+    bool ok = true;
+    uint32_t fixes = 0;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&ctl->kv_full, 2 * C::TILE);
+      for (int c = 0; c < C::ATOMS; ++c) {
+        tma_load_4d(sK + c * kAtom, &mk, &ctl->kv_full, 64 * c, it.k0, it.hk, it.b);
+        tma_load_4d(sV + c * kAtom, &mv, &ctl->kv_full, 64 * c, it.k0, it.hk, it.b);
+      }
+    }
+    int issued = 0;
+    for (int j = 0; j < steps && ok; ++j) {
+      const int s = j & 1, q0 = (it.first + j / a.G) * kTile, h = it.hk * a.G + j % a.G;
+      const bool fix = q0 + kTile > it.len && it.len < a.N;
+      for (int w = 0; w < 2 && ok; ++w) {
+        unsigned char* dst = (w == 0 ? sQ : sO) + s * C::TILE;
+        uint64_t* full = w == 0 ? &ctl->q_full[s] : &ctl->do_full[s];
+        if (j >= 2) ok = __all_sync(0xffffffffu, wait(w == 0 ? &ctl->q_empty[s] : &ctl->do_empty[s], ((j >> 1) - 1) & 1));
+        if (!ok) break;
+        if (w == 0) {
+          const long long row = (static_cast<long long>(it.b) * a.H + h) * a.N;
+          for (int r = lane; r < kTile; r += 32) {
+            const int q = q0 + r;
+            ctl->lse2[s][r] = q < a.N ? a.LSE[row + q] * kLog2e : 0.f;
+            ctl->dq[s][r] = q < a.N ? a.Dq[row + q] : 0.f;
+          }
+          __syncwarp();
+        }
+        uint64_t* bar = fix ? &ctl->fix : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, C::TILE);
+          for (int c = 0; c < C::ATOMS; ++c) tma_load_4d(dst + c * kAtom, w == 0 ? &mq : &mo, bar, 64 * c, q0, h, it.b);
+        }
+        if (fix) {
+          ok = __all_sync(0xffffffffu, wait(&ctl->fix, fixes & 1));
+          ++fixes;
+          if (ok) clear_rows<D>(dst, it.len - q0, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+      }
+      if (ok) issued = j + 1;
+    }
+    // copies in flight must land before the block's shared memory goes away
+    if (lane == 0) {
+      wait_drain(&ctl->kv_full, 0, &g_wbwd_status);
+      for (int s = 0; s < 2; ++s)
+        if (issued > s) {
+          wait_drain(&ctl->q_full[s], ((issued - 1 - s) >> 1) & 1, &g_wbwd_status);
+          wait_drain(&ctl->do_full[s], ((issued - 1 - s) >> 1) & 1, &g_wbwd_status);
+        }
+      if (fixes > 0) wait_drain(&ctl->fix, (fixes - 1) & 1, &g_wbwd_status);
+    }
+  } else if (warp == kMmaWarp && lane == 0) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), o = smem_u32(sO);
+    bool ok = steps > 0 && wait(&ctl->kv_full, 0) && wait(&ctl->q_full[0], 0);
+    if (ok) {
+      tc_fence_after();
+      mma_ss<D>(tmem + T_S, k, q, kIdesc);
+      umma_commit(&ctl->s_full);
+    }
+    for (int j = 0; j < steps && ok; ++j) {
+      const int s = j & 1;
+      if (!(ok = wait(&ctl->do_full[s], (j >> 1) & 1))) break;
+      tc_fence_after();
+      mma_ss<D>(tmem + T_DP, v, o + s * C::TILE, kIdesc);
+      umma_commit(&ctl->dp_full);
+      if (!(ok = wait(&ctl->p_ready, j & 1))) break;
+      tc_fence_after();
+      mma_ts<D>(tmem + T_DV, tmem + T_S, o + s * C::TILE, 8, j > 0);
+      umma_commit(&ctl->do_empty[s]);
+      if (j + 1 < steps) {
+        if (!(ok = wait(&ctl->q_full[s ^ 1], ((j + 1) >> 1) & 1))) break;
+        tc_fence_after();
+        mma_ss<D>(tmem + T_S, k, q + (s ^ 1) * C::TILE, kIdesc);
+        umma_commit(&ctl->s_full);
+      }
+      if (!(ok = wait(&ctl->ds_ready, j & 1))) break;
+      tc_fence_after();
+      mma_ts<D>(tmem + T_DK, tmem + T_DP, q + s * C::TILE, 8, j > 0);
+      umma_commit(&ctl->q_empty[s]);
+    }
+    umma_commit(&ctl->acc_full);  // every MMA issued must complete before TMEM is released
+    wait_drain(&ctl->acc_full, 0, &g_wbwd_status);
+  } else if (warp < 8) {
+    // ---------------------------------------------------------- elementwise
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane, k = it.k0 + row;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t t_s = t_lane + T_S + 64 * half, t_dp = t_lane + T_DP + 64 * half;
+    // of a far chunk only the sinks' rows are used: other warps only keep step
+    const bool idle = it.slot > 0 && it.k0 + quad * 32 >= a.sinks;
+    const bool sink = k < a.sinks;
+    bool ok = true;
+    for (int j = 0; j < steps && ok; ++j) {
+      const int s = j & 1, q0 = (it.first + j / a.G) * kTile;
+      float p[64];
+      // q_full too: it orders the producer's writes of lse2 and dq before their reads
+      ok = __all_sync(0xffffffffu, wait(&ctl->s_full, j & 1) && wait(&ctl->q_full[s], (j >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (!idle) {
+        const bool full = q0 >= it.k0 + kTile - 1 && q0 + kTile <= it.len &&
+                          (q0 + kTile - 1 - it.k0 < a.window || it.k0 + kTile <= a.sinks);
+        tmem_ld64_wait(t_s, p);
+        const float4* l4 = reinterpret_cast<const float4*>(ctl->lse2[s] + 64 * half);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l = l4[c / 4];
+          p[c] = fmaf(p[c], a.scale_log2, -l.x);
+          p[c + 1] = fmaf(p[c + 1], a.scale_log2, -l.y);
+          p[c + 2] = fmaf(p[c + 2], a.scale_log2, -l.z);
+          p[c + 3] = fmaf(p[c + 3], a.scale_log2, -l.w);
+          exp2_four(p[c], p[c + 1], p[c + 2], p[c + 3], (c / 4) % 4 == 3);
+        }
+        if (!full) {
+          // column c is query q0 + 64 half + c; visible from lo to hi
+          const int lo = k - q0 - 64 * half;
+          const int hi = min(sink ? 64 : lo + a.window, it.len - q0 - 64 * half);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < lo || c >= hi) p[c] = 0.f;
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st32_wait(t_s, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_ready);
+      ok = __all_sync(0xffffffffu, wait(&ctl->dp_full, j & 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (!idle) {
+        float x[64];
+        tmem_ld64_wait(t_dp, x);
+        const float4* d4 = reinterpret_cast<const float4*>(ctl->dq[s] + 64 * half);
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 dd = d4[c / 4];
+          // a hidden pair has p = 0, and its dP may be anything
+          const float e0 = p[c] == 0.f ? 0.f : p[c] * (x[c] - dd.x);
+          const float e1 = p[c + 1] == 0.f ? 0.f : p[c + 1] * (x[c + 1] - dd.y);
+          const float e2 = p[c + 2] == 0.f ? 0.f : p[c + 2] * (x[c + 2] - dd.z);
+          const float e3 = p[c + 3] == 0.f ? 0.f : p[c + 3] * (x[c + 3] - dd.w);
+          pk[c / 2] = pack_bf16x2(e0, e1);
+          pk[c / 2 + 1] = pack_bf16x2(e2, e3);
+        }
+        tmem_st32_wait(t_dp, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ds_ready);
+    }
+    if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(&ctl->acc_full, 0));
+    if (ok) {
+      tc_fence_after();
+      const bool zero = steps == 0 || k >= it.len;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t t_acc = t_lane + (w == 0 ? T_DV : T_DK) + half * (D / 2);
+        const float mul = w == 0 ? 1.f : a.scale;
+        if (it.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out[w] + it.b * a.sb[w] + it.hk * a.sh[w] +
+                                                static_cast<long long>(k) * a.sn[w] + half * (D / 2));
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) store_row32(t_acc + c, mul, zero, dst + c / 8, k < a.N);
+        } else {
+          const long long tile = (static_cast<long long>(it.b) * a.Hkv + it.hk) * a.sink_tiles + it.kt;
+          float* dst = a.part + (((tile * (1 + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + half * (D / 2);
+          if (!idle) {
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 32) {
+              uint32_t x[32];
+              tmem_ld32_wait(t_acc + c, x);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!zero)
+                  f = make_float4(__uint_as_float(x[e]) * mul, __uint_as_float(x[e + 1]) * mul,
+                                  __uint_as_float(x[e + 2]) * mul, __uint_as_float(x[e + 3]) * mul);
+                *reinterpret_cast<float4*>(dst + c + e) = f;
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds a sink tile's partial sums in a fixed order: the near queries', then each
+// far chunk's (which hold the sinks' rows only).
+template <int D>
+__global__ void __launch_bounds__(256) sink_kernel(const Args a) {
+  const long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;  // (tile, w, row, 4 channels)
+  constexpr int Q = D / 4;
+  const long long total = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * Q;
+  if (e >= total) return;
+  const int c = static_cast<int>(e % Q);
+  long long r = e / Q;
+  const int row = static_cast<int>(r % kTile);
+  r /= kTile;
+  const int w = static_cast<int>(r % 2);
+  const long long tile = r / 2;
+  const int kt = static_cast<int>(tile % a.sink_tiles), k = kt * kTile + row;
+  if (k >= a.N) return;
+  const long long bh = tile / a.sink_tiles;
+  const int n = k < a.sinks ? 1 + a.chunks : 1;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < n; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(
+        a.part + (((tile * (1 + a.chunks) + i) * 2 + w) * kTile + row) * D + 4 * c);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  const int b = static_cast<int>(bh / a.Hkv), hk = static_cast<int>(bh % a.Hkv);
+  *reinterpret_cast<uint2*>(a.out[w] + b * a.sb[w] + hk * a.sh[w] + static_cast<long long>(k) * a.sn[w] + 4 * c) =
+      make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
+// ----------------------------------------------------------------------- dQ
+struct QCtl {
+  uint64_t q_full[2], q_empty[2], do_full, do_empty;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full, s_free, dp_full, ds_ready;
+  uint64_t dq_full[2], dq_free[2], fix, final_bar;
+  uint32_t tmem_base;
+  volatile int abort;
+};
+
+struct QItem {
+  int b, h, hk, q0, len;
+  int sink_steps, first, steps;
+  __device__ __forceinline__ int key0(int j) const {
+    return (j < sink_steps ? j : first + j - sink_steps) * kTile;
+  }
+};
+
+__device__ __forceinline__ QItem q_item(const Args& a, long long i) {
+  QItem it;
+  const int g = static_cast<int>(i % a.G);
+  long long r = i / a.G;
+  it.q0 = static_cast<int>(r % a.tiles) * kTile;
+  r /= a.tiles;
+  it.hk = static_cast<int>(r % a.Hkv);
+  it.b = static_cast<int>(r / a.Hkv);
+  it.h = it.hk * a.G + g;
+  it.len = length_of(a.lens, it.b, a.N, &g_wbwd_status);
+  it.first = max(0, it.q0 - a.window + 1) / kTile;
+  it.sink_steps = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
+  it.steps = it.q0 < it.len ? it.sink_steps + (min(it.q0 + kTile, it.len) - 1) / kTile - it.first + 1 : 0;
+  return it;
+}
+
+// Steps of this CTA's items, one after another.
+struct QWalk {
+  long long i;
+  QItem it;
+  int j, n;          // step of the item, and the item's number among those with steps
+  bool valid;
+  __device__ __forceinline__ void seek(const Args& a) {
+    for (valid = false; i < a.items; i += gridDim.x) {
+      it = q_item(a, i);
+      if (it.steps > 0) {
+        valid = true;
+        break;
+      }
+    }
+  }
+  __device__ __forceinline__ void begin(const Args& a) {
+    i = blockIdx.x;
+    j = n = 0;
+    seek(a);
+  }
+  __device__ __forceinline__ void next(const Args& a) {
+    if (++j < it.steps) return;
+    j = 0;
+    ++n;
+    i += gridDim.x;
+    seek(a);
+  }
+  __device__ __forceinline__ bool last() const { return j + 1 == it.steps; }
+  // a sink tile outside the window that shows at most 32 keys takes 32 columns
+  __device__ __forceinline__ bool narrow(const Args& a) const {
+    return j < it.sink_steps && a.sinks - j * kTile <= 32;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args a) {
+  using C = Cfg<D>;
+  constexpr int T_S = 0, T_DP = 128, T_DQ = 256;  // two dQ, D columns each
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_wbwd_status, BSA_STATUS_INTERNAL);
+    return;
+  }
+  unsigned char *sQ = smem, *sO = smem + 2 * C::TILE, *sK = smem + 3 * C::TILE, *sV = smem + 5 * C::TILE;
+  QCtl* ctl = reinterpret_cast<QCtl*>(smem + 7 * C::TILE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_empty[s], 1);
+      mbar_init(&ctl->k_full[s], 1);
+      mbar_init(&ctl->k_empty[s], 1);
+      mbar_init(&ctl->v_full[s], 1);
+      mbar_init(&ctl->v_empty[s], 1);
+      mbar_init(&ctl->dq_full[s], 1);
+      mbar_init(&ctl->dq_free[s], 8);
+    }
+    mbar_init(&ctl->do_full, 1);
+    mbar_init(&ctl->do_empty, 1);
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->s_free, 8);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->ds_ready, 8);
+    mbar_init(&ctl->fix, 1);
+    mbar_init(&ctl->final_bar, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return wait_bounded(bar, parity, &ctl->abort, &g_wbwd_status);
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------- producer
+    QWalk w;
+    w.begin(a);
+    bool ok = true;
+    uint32_t t = 0, items = 0, fixes = 0;  // steps, items whose tiles were issued
+    for (; w.valid && ok; w.next(a)) {
+      if (w.j == 0) {
+        const int s = w.n & 1;
+        if (w.n >= 2) ok = warp_wait(&ctl->q_empty[s], ((w.n >> 1) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl->q_full[s], C::TILE);
+          for (int c = 0; c < C::ATOMS; ++c)
+            tma_load_4d(sQ + s * C::TILE + c * kAtom, &mq, &ctl->q_full[s], 64 * c, w.it.q0, w.it.h, w.it.b);
+        }
+      }
+      const int k0 = w.it.key0(w.j), s = t & 1;
+      const bool fix = k0 + kTile > w.it.len && w.it.len < a.N;  // dS K: key rows past the end must be 0
+      if (t >= 2) ok = warp_wait(&ctl->k_empty[s], ((t >> 1) - 1) & 1);
+      if (!ok) break;
+      {
+        uint64_t* bar = fix ? &ctl->fix : &ctl->k_full[s];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, C::TILE);
+          for (int c = 0; c < C::ATOMS; ++c)
+            tma_load_4d(sK + s * C::TILE + c * kAtom, &mk, bar, 64 * c, k0, w.it.hk, w.it.b);
+        }
+        if (fix) {
+          ok = warp_wait(&ctl->fix, fixes & 1);
+          ++fixes;
+          if (ok) clear_rows<D>(sK + s * C::TILE, w.it.len - k0, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->k_full[s]);
+        }
+      }
+      if (w.j == 0) {
+        if (w.n >= 1) ok = ok && warp_wait(&ctl->do_empty, (w.n - 1) & 1);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&ctl->do_full, C::TILE);
+          for (int c = 0; c < C::ATOMS; ++c)
+            tma_load_4d(sO + c * kAtom, &mo, &ctl->do_full, 64 * c, w.it.q0, w.it.h, w.it.b);
+        }
+        if (ok) ++items;
+      }
+      if (t >= 2) ok = ok && warp_wait(&ctl->v_empty[s], ((t >> 1) - 1) & 1);
+      if (ok && lane == 0) {
+        mbar_arrive_expect_tx(&ctl->v_full[s], C::TILE);
+        for (int c = 0; c < C::ATOMS; ++c)
+          tma_load_4d(sV + s * C::TILE + c * kAtom, &mv, &ctl->v_full[s], 64 * c, k0, w.it.hk, w.it.b);
+      }
+      if (ok) ++t;
+    }
+    if (lane == 0) {
+      for (uint32_t s = 0; s < 2; ++s) {
+        if (t > s) {
+          wait_drain(&ctl->k_full[s], ((t - 1 - s) >> 1) & 1, &g_wbwd_status);
+          wait_drain(&ctl->v_full[s], ((t - 1 - s) >> 1) & 1, &g_wbwd_status);
+        }
+        if (items > s) wait_drain(&ctl->q_full[s], ((items - 1 - s) >> 1) & 1, &g_wbwd_status);
+      }
+      if (items > 0) wait_drain(&ctl->do_full, (items - 1) & 1, &g_wbwd_status);
+      if (fixes > 0) wait_drain(&ctl->fix, (fixes - 1) & 1, &g_wbwd_status);
+    }
+  } else if (warp == kMmaWarp && lane == 0) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), o = smem_u32(sO);
+    auto idesc = [&](bool narrow) {
+      return narrow ? idesc_bf16_f32(128, 32, false, false) : idesc_bf16_f32(128, 128, false, false);
+    };
+    auto scores = [&](const QWalk& w, uint32_t t) {  // S of step t, the step w stands at
+      if (w.j == 0 && !wait(&ctl->q_full[w.n & 1], (w.n >> 1) & 1)) return false;
+      if (t > 0 && !wait(&ctl->s_free, (t - 1) & 1)) return false;
+      if (!wait(&ctl->k_full[t & 1], (t >> 1) & 1)) return false;
+      tc_fence_after();
+      mma_ss<D>(tmem + T_S, q + (w.n & 1) * C::TILE, k + (t & 1) * C::TILE, idesc(w.narrow(a)));
+      umma_commit(&ctl->s_full);
+      if (w.last()) umma_commit(&ctl->q_empty[w.n & 1]);
+      return true;
+    };
+    QWalk w;
+    w.begin(a);
+    bool ok = !w.valid || scores(w, 0);
+    for (uint32_t t = 0; w.valid && ok; ++t) {
+      const int s = t & 1;
+      ok = (w.j > 0 || wait(&ctl->do_full, w.n & 1)) && wait(&ctl->v_full[s], (t >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      mma_ss<D>(tmem + T_DP, o, v + s * C::TILE, idesc(w.narrow(a)));
+      umma_commit(&ctl->dp_full);
+      umma_commit(&ctl->v_empty[s]);
+      if (w.last()) umma_commit(&ctl->do_empty);
+      QWalk nx = w;
+      nx.next(a);
+      if (nx.valid && !(ok = scores(nx, t + 1))) break;
+      const int buf = w.n & 1;
+      if (w.j == 0 && w.n >= 2 && !(ok = wait(&ctl->dq_free[buf], ((w.n >> 1) - 1) & 1))) break;
+      if (!(ok = wait(&ctl->ds_ready, t & 1))) break;
+      tc_fence_after();
+      mma_ts<D>(tmem + T_DQ + buf * D, tmem + T_DP, k + s * C::TILE, w.narrow(a) ? 2 : 8, w.j > 0);
+      umma_commit(&ctl->k_empty[s]);
+      if (w.last()) umma_commit(&ctl->dq_full[buf]);
+      w = nx;
+    }
+    umma_commit(&ctl->final_bar);
+    wait_drain(&ctl->final_bar, 0, &g_wbwd_status);
+  } else if (warp < 8) {
+    // ---------------------------------------------------------- elementwise
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t t_s = t_lane + T_S + 64 * half, t_dp = t_lane + T_DP + 64 * half;
+    // tiles without a visible pair first: nothing in flight depends on them
+    for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+      const QItem it = q_item(a, i);
+      if (it.steps > 0 || it.q0 + row >= a.N) continue;
+      uint4* dst = reinterpret_cast<uint4*>(a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] +
+                                            static_cast<long long>(it.q0 + row) * a.sn[0] + half * (D / 2));
+      for (int c = 0; c < D / 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    auto store = [&](const QItem& it, int n) {  // dQ of the n-th item
+      const int buf = n & 1, q = it.q0 + row;
+      if (!warp_wait(&ctl->dq_full[buf], (n >> 1) & 1)) return false;
+      tc_fence_after();
+      uint4* dst = reinterpret_cast<uint4*>(a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] +
+                                            static_cast<long long>(q) * a.sn[0] + half * (D / 2));
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32)
+        store_row32(t_lane + T_DQ + buf * D + half * (D / 2) + c, a.scale, q >= it.len, dst + c / 8, q < a.N);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->dq_free[buf]);
+      return true;
+    };
+    QWalk w;
+    w.begin(a);
+    QItem prev = w.it;
+    bool ok = true;
+    float lse2 = 0.f, dd = 0.f;
+    for (uint32_t t = 0; w.valid && ok; ++t) {
+      const QItem& it = w.it;
+      const int q = it.q0 + row, k0 = it.key0(w.j);
+      if (w.j == 0) {
+        const long long at = (static_cast<long long>(it.b) * a.H + it.h) * a.N + q;
+        lse2 = q < it.len ? a.LSE[at] * kLog2e : 0.f;
+        dd = q < it.len ? a.Dq[at] : 0.f;
+      }
+      const bool narrow = w.narrow(a);
+      const bool work = !narrow || half == 0;
+      float p[64];
+      if (!(ok = warp_wait(&ctl->s_full, t & 1))) break;
+      tc_fence_after();
+      if (work) {
+        if (narrow)
+          tmem_ld32lo_wait(t_s, p);
+        else
+          tmem_ld64_wait(t_s, p);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->s_free);
+      if (work) {
+        const bool full = k0 + kTile - 1 <= it.q0 && it.q0 + kTile <= it.len &&
+                          (k0 > it.q0 + kTile - 1 - a.window || k0 + kTile <= a.sinks);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          fma2(p[c], p[c + 1], a.scale_log2, -lse2);
+          fma2(p[c + 2], p[c + 3], a.scale_log2, -lse2);
+          exp2_four(p[c], p[c + 1], p[c + 2], p[c + 3], (c / 4) % 4 == 3);
+        }
+        if (!full) {
+          // column c is key k0 + 64 half + c
+          const int hi = q < it.len ? q - k0 - 64 * half : -1;
+          const int lo = q - a.window + 1 - k0 - 64 * half, sk = a.sinks - k0 - 64 * half;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c > hi || (c < lo && c >= sk)) p[c] = 0.f;
+        }
+      }
+      if (!(ok = warp_wait(&ctl->dp_full, t & 1))) break;
+      tc_fence_after();
+      if (work) {
+        float x[64];
+        if (narrow)
+          tmem_ld32lo_wait(t_dp, x);
+        else
+          tmem_ld64_wait(t_dp, x);
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          // a hidden pair has p = 0, and its dP may be anything
+          const float e0 = p[c] == 0.f ? 0.f : p[c] * (x[c] - dd);
+          const float e1 = p[c + 1] == 0.f ? 0.f : p[c + 1] * (x[c + 1] - dd);
+          pk[c / 2] = pack_bf16x2(e0, e1);
+        }
+        tmem_st32_wait(t_dp, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ds_ready);
+      // the last tile's dQ is stored here, beside this tile's products
+      if (w.j == 0 && w.n > 0 && !(ok = store(prev, w.n - 1))) break;
+      if (w.last()) {
+        prev = w.it;
+        const int n = w.n;
+        w.next(a);
+        if (!w.valid) ok = store(prev, n);
+      } else {
+        w.next(a);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+// How the far queries of the sinks are cut: into chunks of about a near tile's
+// length, at most kMaxChunks.
+struct Plan {
+  int tiles, sink_tiles, chunks, chunk_tiles;
+  size_t d_bytes, part_bytes;
+};
+
+Plan make_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  Plan p;
+  const long long w = window < N ? window : N, s = sinks < N ? sinks : N;
+  p.tiles = (N + kTile - 1) / kTile;
+  // near query tiles of key tile t end at t + (kTile - 1 + w - 1) / kTile
+  const long long near = (kTile + w - 2) / kTile;
+  const long long far = p.tiles - 1 - near;  // far query tiles of key tile 0
+  p.sink_tiles = p.chunks = p.chunk_tiles = 0;
+  if (far > 0 && s > 0) {
+    const long long st = (s + kTile - 1) / kTile;
+    p.sink_tiles = static_cast<int>(st < far ? st : far);  // tile t has far - t of them
+    long long n = (far + near) / (near + 1);
+    n = n < 1 ? 1 : (n > kMaxChunks ? kMaxChunks : n);
+    p.chunk_tiles = static_cast<int>((far + n - 1) / n);
+    p.chunks = static_cast<int>((far + p.chunk_tiles - 1) / p.chunk_tiles);
+  }
+  const size_t rows = static_cast<size_t>(B) * H * N;
+  p.d_bytes = (rows * 4 + 255) / 256 * 256;
+  p.part_bytes = static_cast<size_t>(B) * Hkv * p.sink_tiles * (1 + p.chunks) * 2 * kTile * d * 4;
+  return p;
+}
+
+template <int D>
+int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_view* o, const bsa_view* g,
+           Args a, float* Dq, const bsa_view* dq, const bsa_view* dk, const bsa_view* dv, cudaStream_t s) {
+  using C = Cfg<D>;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_map(&mq, q, a.B, a.H, a.N, D) || !make_map(&mk, k, a.B, a.Hkv, a.N, D) ||
+      !make_map(&mv, v, a.B, a.Hkv, a.N, D) || !make_map(&mo, g, a.B, a.H, a.N, D))
+    return BSA_ERR_CUDA;
+  // One CTA (and its 512 TMEM columns) per SM: more than half an SM's shared memory.
+  int kv_smem = 6 * C::TILE + static_cast<int>(sizeof(KvCtl)), q_smem = 7 * C::TILE + static_cast<int>(sizeof(QCtl));
+  kv_smem = kv_smem < 120 * 1024 ? 120 * 1024 : kv_smem;
+  q_smem = q_smem < 120 * 1024 ? 120 * 1024 : q_smem;
+  if (cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem) != cudaSuccess ||
+      cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  auto stride = [](int n, long long x) { return n > 1 ? x : 0; };
+
+  DotArgs d;
+  d.o = static_cast<const __nv_bfloat16*>(o->data);
+  d.g = static_cast<const __nv_bfloat16*>(g->data);
+  d.osb = stride(a.B, o->stride_b), d.osh = stride(a.H, o->stride_h), d.osn = stride(a.N, o->stride_n);
+  d.gsb = stride(a.B, g->stride_b), d.gsh = stride(a.H, g->stride_h), d.gsn = stride(a.N, g->stride_n);
+  d.D = Dq;
+  d.rows = static_cast<long long>(a.B) * a.H * a.N;
+  d.H = a.H;
+  d.N = a.N;
+  const long long per = 8 * (32 / (D / 8)), blocks = (d.rows + per - 1) / per;
+  const long long kv_items = static_cast<long long>(a.B) * a.Hkv * (a.tiles + static_cast<long long>(a.sink_tiles) * a.chunks);
+  const long long q_items = static_cast<long long>(a.B) * a.H * a.tiles;
+  const long long sink_elems = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * (D / 4);
+  if (blocks > 0x7fffffffLL || kv_items > 0x7fffffffLL || sink_elems / 256 > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;
+  dot_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(d);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+
+  Args kv = a;
+  const bsa_view* outs[2] = {dv, dk};
+  for (int w = 0; w < 2; ++w) {
+    kv.out[w] = static_cast<__nv_bfloat16*>(const_cast<void*>(outs[w]->data));
+    kv.sb[w] = stride(a.B, outs[w]->stride_b);
+    kv.sh[w] = stride(a.Hkv, outs[w]->stride_h);
+    kv.sn[w] = stride(a.N, outs[w]->stride_n);
+  }
+  kv.items = kv_items;
+  dkdv_kernel<D><<<static_cast<unsigned>(kv_items), kThreads, kv_smem, s>>>(mq, mk, mv, mo, kv);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  if (a.sink_tiles > 0) {
+    sink_kernel<D><<<static_cast<unsigned>((sink_elems + 255) / 256), 256, 0, s>>>(kv);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  }
+
+  Args qa = a;
+  qa.out[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(dq->data));
+  qa.sb[0] = stride(a.B, dq->stride_b);
+  qa.sh[0] = stride(a.H, dq->stride_h);
+  qa.sn[0] = stride(a.N, dq->stride_n);
+  qa.items = q_items;
+  const long long sms = sm_count();
+  dq_kernel<D><<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, q_smem, s>>>(mq, mk, mv, mo, qa);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace wbwd
+
+int take_status(const void* symbol, uint32_t* status, int clear);
+int window_backward_status(uint32_t* status, int clear) {
+  return take_status(&wbwd::g_wbwd_status, status, clear);
+}
+}  // namespace bsa
+
+extern "C" size_t bsa_window_backward_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || N < 1 || (d != 64 && d != 128) || window < 1 || sinks < 0) return 0;
+  const auto p = bsa::wbwd::make_plan(B, H, Hkv, N, d, window, sinks);
+  return p.d_bytes + p.part_bytes;
+}
+
+extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_view* o,
+                                   const bsa_view* dO, const float* LSE, const int32_t* lens, int B, int H, int Hkv,
+                                   int N, int d, int window, int sinks, float scale, const bsa_view* dq,
+                                   const bsa_view* dk, const bsa_view* dv, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  using namespace bsa::wbwd;
+  if (B < 1 || H < 1 || Hkv < 1 || N < 1 || d < 1 || H % Hkv != 0 || window < 1 || sinks < 0 ||
+      !std::isfinite(scale) || !LSE || (reinterpret_cast<uintptr_t>(LSE) & 3u) != 0 || !workspace ||
+      (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+    return BSA_ERR_INVALID_ARG;
+  if (!view_ok(q, B, H, N, d) || !view_ok(k, B, Hkv, N, d) || !view_ok(v, B, Hkv, N, d) || !view_ok(o, B, H, N, d) ||
+      !view_ok(dO, B, H, N, d) || !view_ok(dq, B, H, N, d) || !view_ok(dk, B, Hkv, N, d) || !view_ok(dv, B, Hkv, N, d))
+    return BSA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  if (N > (1 << 30)) return BSA_ERR_UNSUPPORTED;
+  const Plan p = make_plan(B, H, Hkv, N, d, window, sinks);
+  if (workspace_bytes < p.d_bytes + p.part_bytes) return BSA_ERR_BUFFER_TOO_SMALL;
+  Args a = {};
+  a.lens = lens;
+  a.LSE = LSE;
+  a.Dq = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.d_bytes);
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.N = N;
+  a.tiles = p.tiles;
+  a.window = window < N ? window : N;
+  a.sinks = sinks < N ? sinks : N;
+  a.sink_tiles = p.sink_tiles;
+  a.chunks = p.chunks;
+  a.chunk_tiles = p.chunk_tiles;
+  a.scale = scale;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* D = static_cast<float*>(workspace);
+  return d == 64 ? launch<64>(q, k, v, o, dO, a, D, dq, dk, dv, s) : launch<128>(q, k, v, o, dO, a, D, dq, dk, dv, s);
+}

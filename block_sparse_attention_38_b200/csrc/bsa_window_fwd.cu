@@ -28,7 +28,7 @@
 //
 // Softmax: maxima on raw scores, lazy rescale of O (only when the maximum grows by
 // more than 2^8, so P <= 2^8), 2^x with the scale folded in, part of it by a
-// polynomial on the FMA pipe.  P is rounded to bf16 (2^-9 relative, like the
+// polynomial on the FMA pipe.  P is rounded to bf16 (2^-8 at most, like the
 // operands it meets); maxima, sums and O are fp32.
 //
 // Every wait is bounded.

@@ -36,9 +36,13 @@ def _declare(lib) -> None:
             ("bsa_q4_window_decode", [_vp, _vp, _vp, cache, _vp, i, i, i, f, _vp, _vp, _vp]),
             ("bsa_window_decode", [_vp] * 6 + [i] * 7 + [f, _vp, _vp, _vp]),
             ("bsa_window_forward", [view] * 3 + [_vp] + [i] * 7 + [f, view, _vp, _vp]),
+            ("bsa_window_backward", [view] * 5 + [_vp, _vp] + [i] * 7 + [f] + [view] * 3
+             + [_vp, ctypes.c_size_t, _vp]),
             ("bsa_stream_status", [ctypes.POINTER(ctypes.c_uint32), i])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, types
+    lib.bsa_window_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.bsa_window_backward_workspace_bytes.argtypes = [i] * 7
 
 
 class Q4Cache(NamedTuple):
@@ -274,6 +278,46 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] 
           Hkv, N, d, int(window), int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
           _view("out", out, (B, H, N, d), device), _rows("lse", lse, (B, H, N), device, torch.float32))
     return out, lse
+
+
+def window_backward_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, window: int, sinks: int = 0) -> int:
+    """Workspace bytes `window_backward` needs for these sizes."""
+    n = int(library().bsa_window_backward_workspace_bytes(B, H, Hkv, N, d, window, sinks))
+    if n == 0:
+        raise ValueError("no workspace for these sizes: check H % Hkv, d in (64, 128), window >= 1, sinks >= 0")
+    return n
+
+
+def window_backward(q, k, v, o, do, lse, window: int, sinks: int = 0, scale: Optional[float] = None, lens=None,
+                    workspace=None):
+    """Gradients of `window_forward` (bsa_window_backward): (dQ like q, dK like k,
+    dV like v) for the gradient do of its output o; lse as it returned it (copied
+    first where it is not contiguous).
+
+    workspace: a CUDA tensor of at least window_backward_workspace_bytes(...)
+    bytes (allocated on the current stream when not given); calls that may run
+    at the same time need one each.
+    """
+    import torch
+
+    B, H, Hkv, N, d = _heads(q, k)
+    device = q.device
+    qs, ks = (B, H, N, d), (B, Hkv, N, d)
+    views = [_view(n, t, s, device) for n, t, s in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs),
+                                                    ("do", do, qs))]
+    lse = lse.contiguous()
+    lp = _rows("lse", lse, (B, H, N), device, torch.float32)
+    nbytes = window_backward_workspace_bytes(B, H, Hkv, N, d, int(window), int(sinks))
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    _call(device, "bsa_window_backward", *views, lp, None if lens is None else _ints("lens", lens, B, device), B, H,
+          Hkv, N, d, int(window), int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+          _view("dq", dq, qs, device), _view("dk", dk, ks, device), _view("dv", dv, ks, device),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dv
 
 
 def stream_status(clear: bool = True) -> int:

@@ -475,6 +475,28 @@ int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v, 
                        int H, int Hkv, int N, int d, int window, int sinks, float scale, const bsa_view* o,
                        float* LSE, void* stream);
 
+/*
+ * bsa_window_backward -- gradients of bsa_window_forward.  With
+ * P = exp(scale q.k - LSE) over the visible pairs and D = dO . O for each query:
+ * dV = sum P dO, dS = P (dO.v - D), dQ = scale sum dS k, dK = scale sum dS q; the
+ * sums for dK and dV run over the query heads that share the head too.
+ *
+ * q, o, dO, dq: [B, H, N, d] views; k, v, dk, dv: [B, Hkv, N, d] views (o and LSE
+ * from bsa_window_forward on the same q, k, v, lens, window, sinks and scale).
+ * dq, dk, dv are written in full; rows from lens[b] on are 0, whatever the inputs
+ * hold there.  workspace: device memory of at least
+ * bsa_window_backward_workspace_bytes(...) bytes, 16-byte aligned, which the call
+ * overwrites; calls that may run at the same time need one each.  Enqueued on
+ * `stream` (three launches, four with far queries of sinks); nothing allocated or
+ * synchronised; no atomics, so the same bits every run.  Supported values, lens
+ * and strides as for the forward; BSA_ERR_BUFFER_TOO_SMALL for a short workspace.
+ */
+size_t bsa_window_backward_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks);
+int bsa_window_backward(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_view* o,
+                        const bsa_view* dO, const float* LSE, const int32_t* lens, int B, int H, int Hkv, int N,
+                        int d, int window, int sinks, float scale, const bsa_view* dq, const bsa_view* dk,
+                        const bsa_view* dv, void* workspace, size_t workspace_bytes, void* stream);
+
 /* bsa_stream_status -- as bsa_device_status, for the status words of the
  * functions of this section. */
 int bsa_stream_status(uint32_t* status, int clear);

@@ -136,13 +136,19 @@ def window_forward(q, k, v, window, sinks, scale, lens=None):
     return O, L
 
 
-def window_backward(q, k, v, do, window, sinks, scale, lens=None):
-    """(dQ, dK, dV) of window_forward for the output gradient do, by the chain rule."""
+def window_backward(q, k, v, do, window, sinks, scale, lens=None, magnitudes=False):
+    """(dQ, dK, dV) of window_forward for the output gradient do, by the chain rule.
+
+    With magnitudes also, for each element, the sum of its terms' magnitudes, and
+    what a relative error of 1 in every O element and in every term of the sum that
+    it is can move the element by (through D = dO . O).
+    """
     O, L = window_forward(q, k, v, window, sinks, scale, lens)
     q, k, v, do = _f64(q), _f64(k), _f64(v), _f64(do)
     B, H, N, d = q.shape
     G = H // k.shape[1]
     dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    size, moved = [np.zeros(x.shape) for x in (q, k, v)], [np.zeros(x.shape) for x in (q, k, v)]
     for b in range(B):
         n = N if lens is None else int(lens[b])
         if n == 0:
@@ -157,4 +163,11 @@ def window_backward(q, k, v, do, window, sinks, scale, lens=None):
             dq[b, h, :n] = ds @ k[b, c, :n]
             dk[b, c, :n] += ds.T @ q[b, h, :n]
             dv[b, c, :n] += p.T @ g
-    return dq, dk, dv
+            if magnitudes:
+                weight = np.abs(O[b, h, :n]) + p @ np.abs(v[b, c, :n])
+                e = p * (np.abs(g) * weight).sum(-1, keepdims=True) * abs(scale)
+                size[0][b, h, :n], moved[0][b, h, :n] = np.abs(ds) @ np.abs(k[b, c, :n]), e @ np.abs(k[b, c, :n])
+                size[1][b, c, :n] += np.abs(ds).T @ np.abs(q[b, h, :n])
+                moved[1][b, c, :n] += e.T @ np.abs(q[b, h, :n])
+                size[2][b, c, :n] += p.T @ np.abs(g)
+    return ((dq, dk, dv), size, moved) if magnitudes else (dq, dk, dv)

@@ -139,3 +139,79 @@ def test_quantising_by_hand():
     assert code[0, 0] == 0 and code[0, 31] == 15 and code[0, 1] == 0 and code[0, 2] == 1
     assert s[0, 1] == 0 and m[0, 1] == -3 and (code[0, 32:] == 0).all()
     assert np.abs(o.values(code, s, m) - x).max() <= 0.5 * s[0, 0] + 15 * 2.0 ** -11 * s[0, 0]
+
+
+# ------------------------------------------------------- sliding-window attention
+def _v(data=P, b=64, h=64, n=64):
+    return ls._View(data, b, h, n)
+
+
+SIZES = dict(B=2, H=6, Hkv=3, N=40, d=64, window=8, sinks=2, scale=0.1, LSE=P)
+BAD_SIZES = [dict(B=0), dict(H=0), dict(Hkv=0), dict(H=7), dict(N=0), dict(d=0), dict(window=0), dict(sinks=-1),
+             dict(scale=NAN), dict(LSE=None), dict(LSE=P + 2)]
+BAD_VIEWS = [_v(None), _v(P8), _v(b=4), _v(h=60), _v(n=65), _v(n=0), _v(n=32), _v(b=-64), _v(n=1 << 39)]
+
+
+def _forward(bad=None, at=0, **kw):
+    a = dict(SIZES, **kw)
+    v = [_v() for _ in range(4)]
+    if bad is not None:
+        v[at] = bad
+    return bsa.library().bsa_window_forward(v[0], v[1], v[2], None, a["B"], a["H"], a["Hkv"], a["N"], a["d"],
+                                            a["window"], a["sinks"], a["scale"], v[3], a["LSE"], None)
+
+
+def _backward(bad=None, at=0, ws=P, nbytes=1 << 30, **kw):
+    a = dict(SIZES, **kw)
+    v = [_v() for _ in range(8)]
+    if bad is not None:
+        v[at] = bad
+    return bsa.library().bsa_window_backward(*v[:5], a["LSE"], None, a["B"], a["H"], a["Hkv"], a["N"], a["d"],
+                                             a["window"], a["sinks"], a["scale"], *v[5:], ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw", BAD_SIZES, ids=_ids)
+def test_window_sizes(kw):
+    assert _forward(**kw) == bsa.ERR_INVALID_ARG
+    assert _backward(**kw) == bsa.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", range(len(BAD_VIEWS)))
+def test_window_views(bad):
+    for at in range(4):
+        assert _forward(BAD_VIEWS[bad], at) == bsa.ERR_INVALID_ARG
+    for at in range(8):
+        assert _backward(BAD_VIEWS[bad], at) == bsa.ERR_INVALID_ARG
+
+
+def test_window_unsupported_and_workspace():
+    wide = [ls._View(P, 96, 96, 96) for _ in range(8)]
+    lib = bsa.library()
+    assert lib.bsa_window_forward(*wide[:3], None, 2, 6, 3, 40, 96, 8, 2, 0.1, wide[3], P, None) == bsa.ERR_UNSUPPORTED
+    assert lib.bsa_window_backward(*wide[:5], P, None, 2, 6, 3, 40, 96, 8, 2, 0.1, *wide[5:], P, 1 << 30,
+                                   None) == bsa.ERR_UNSUPPORTED
+    need = bsa.window_backward_workspace_bytes(2, 6, 3, 40, 64, 8, 2)
+    assert _backward(nbytes=need - 1) == bsa.ERR_BUFFER_TOO_SMALL
+    assert _backward(ws=None) == _backward(ws=P8) == bsa.ERR_INVALID_ARG
+
+
+def test_workspace_sizes():
+    size = bsa.window_backward_workspace_bytes
+    assert size(1, 1, 1, 1, 64, 1) >= 4
+    assert size(1, 4, 2, 4096, 128, 256, 4) > size(1, 4, 2, 4096, 128, 256, 0) >= 4 * 4 * 4096
+    assert size(1, 4, 2, 4096, 128, 4096, 4) == size(1, 4, 2, 4096, 128, 4096, 0)  # no far queries
+    # sinks cost two rows-times-channels sums for each chunk, whatever the length
+    assert size(1, 1, 1, 1 << 20, 128, 128, 4) < 4 * (1 << 20) + (2 + 32) * 2 * 128 * 128 * 4
+    for bad in ((1, 3, 2, 8, 64, 1), (1, 1, 1, 8, 96, 1), (1, 1, 1, 8, 64, 0), (0, 1, 1, 8, 64, 1)):
+        with pytest.raises(ValueError):
+            size(*bad)
+
+
+def test_binding_refuses_cpu_and_broadcast_tensors():
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        bsa.window_forward(x, x, x, 2)
+    with pytest.raises(ValueError):
+        bsa.window_forward(torch.zeros(1, 3, 3, 64, dtype=torch.bfloat16), x, x, 2)
+    with pytest.raises(ValueError):
+        bsa.window_backward(x, x, x, x, x, torch.zeros(1, 2, 3), 2)

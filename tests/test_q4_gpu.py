@@ -65,8 +65,8 @@ def test_write_and_read(B, H, T, L, d, kind):
             for got, x in ((kr, k), (vr, v)):
                 want = o.values(*o.quantise(x[b, h, :n]))
                 got = got[b, h].float().cpu().numpy()
-                # one rounding of the fp32 sum (2^-24) and one to bf16 (2^-9 of the value)
-                np.testing.assert_allclose(got[:n], want, rtol=2.0 ** -8, atol=1e-30)
+                # one rounding of the fp32 sum (2^-24 of the value) and one to bf16 (2^-8)
+                np.testing.assert_allclose(got[:n], want, rtol=2.0 ** -8 + 2.0 ** -20, atol=1e-30)
                 assert (got[n:] == 0).all()
 
 
@@ -98,7 +98,7 @@ def test_nan_and_infinity_stay_in_their_group():
     want = o.values(*o.quantise(k[0, 0]))
     assert np.isnan(got[1, :32]).all() and np.isfinite(got[1, 32:]).all()
     assert np.isfinite(got[2]).all()
-    np.testing.assert_allclose(got, want, rtol=2.0 ** -8)
+    np.testing.assert_allclose(got, want, rtol=2.0 ** -8 + 2.0 ** -20)
 
 
 def test_bad_ranges_are_reported_and_leave_the_cache():
@@ -127,8 +127,8 @@ def test_rows_past_two_to_the_31_bytes():
     bsa.q4_write(cache, k.cuda(), k.cuda(), start)
     kr, vr = bsa.q4_read(cache, start, 3)
     want = o.values(*o.quantise(k))
-    np.testing.assert_allclose(kr.float().cpu().numpy(), want, rtol=2.0 ** -8)
-    np.testing.assert_allclose(vr.float().cpu().numpy(), want, rtol=2.0 ** -8)
+    np.testing.assert_allclose(kr.float().cpu().numpy(), want, rtol=2.0 ** -8 + 2.0 ** -20)
+    np.testing.assert_allclose(vr.float().cpu().numpy(), want, rtol=2.0 ** -8 + 2.0 ** -20)
     q = torch.randn(B, H, d).to(torch.bfloat16)
     n = torch.tensor([L], dtype=torch.int32, device="cuda")
     got, lse = bsa.q4_window_decode(q.cuda(), cache, n, window=3)

@@ -1,11 +1,13 @@
 """Sliding-window attention on the GPU against the fp64 oracle.
 
-Tolerances of the forward.  P is rounded to bf16 before P V and O after it, each
-off by at most 2^-9 of the value; part of the exponentials is taken to 7.5e-5.  So
-|O - exact| <= 2^-9 |O| + (2^-9 + 1.5e-4) sum_k p_k |v_k| + fp32 terms, and
-sum_k p_k |v_k| <= max |v|: 2^-8 |O| + 2^-8 max |v| holds them with the fp32
-scores' share (x to 2^-20 of its largest term, below 2^-11 of a weight).  LSE:
-the sum's relative error, at most 7.5e-5 plus the scores' error, below 2^-12.
+Tolerances of the forward.  bf16 rounding is off by at most 2^-8 of the value
+(half a step); P is rounded so before P V and O after it, and part of the
+exponentials is taken to 7.5e-5.  The errors of P's many terms are independent, so
+|O - exact| <= 2^-8 |O| + 2^-8 max |v|: sum_k p_k |v_k| <= max |v|, of which the
+rounding of P alone can take 2^-8 only if every term is off by half a step the
+same way, and the fp32 scores' share (x to 2^-20 of its largest term) and the
+polynomial's fit into what that leaves.  LSE: the sum's relative error, at most
+7.5e-5 plus the scores' error, below 2^-12.
 """
 import numpy as np
 import pytest
