@@ -40,8 +40,9 @@ namespace wfwd {
 using namespace bsa::win;
 
 constexpr int kSlots = 2;
-constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kSoftWarps = 16;                 // 8 per slot: two per TMEM lane quadrant
+constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kThreads = 18 * 32;
 constexpr float kRescale = 8.f;  // log2 units
 
 __device__ unsigned int g_wfwd_status;
@@ -62,11 +63,10 @@ struct Ctl {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[kSlots], p_full[kSlots];
   uint64_t o_full[kSlots], o_free[kSlots];
-  uint64_t ml_full[kSlots], ml_free[kSlots];
   uint64_t fix, final_bar;
   uint32_t tmem_base;
   volatile int abort;
-  float2 ml[kSlots][kTile];  // (maximum in log2 units, sum) of each row
+  float row[kSlots][2][kTile];  // exchange between the two threads of a row
 };
 
 struct Args {
@@ -74,47 +74,45 @@ struct Args {
   __nv_bfloat16* O;
   long long o_sb, o_sh, o_sn;
   float* LSE;
-  int B, H, Hkv, G, N;
-  int pairs;          // items per tile row of a cached head (G even: G / 2; else G)
-  int rows;           // tile rows: q tiles (G even) or pairs of them
+  int B, H, G, N;
+  unsigned Hkv;
+  unsigned pairs;     // items per tile row of a cached head (G even: G / 2; else G)
+  unsigned rows;      // tile rows: q tiles (G even) or pairs of them
   int by_head;        // the two slots are two heads
   int window, sinks;
-  long long items;
+  unsigned items;
   float scale_log2;
 };
 
 struct Item {
   int b, hk, len;
-  int h[kSlots], q0[kSlots];
+  int h0, dh, q00, dq;  // slot 0's head and first query, and how far slot 1's are on
   int sink_steps, first, steps;
+  __device__ __forceinline__ int h(int s) const { return h0 + s * dh; }
+  __device__ __forceinline__ int q0(int s) const { return q00 + s * dq; }
   __device__ __forceinline__ int key0(int j) const {
     return (j < sink_steps ? j : first + j - sink_steps) * kTile;
   }
 };
 
-__device__ __forceinline__ Item item_of(const Args& a, long long i) {
+__device__ __forceinline__ Item item_of(const Args& a, unsigned i) {
   Item it;
-  const int p = static_cast<int>(i % a.pairs);
-  long long r = i / a.pairs;
-  const int row = static_cast<int>(r % a.rows);
-  r /= a.rows;
-  it.hk = static_cast<int>(r % a.Hkv);
-  it.b = static_cast<int>(r / a.Hkv);
-  if (a.by_head) {
-    it.h[0] = it.hk * a.G + 2 * p;
-    it.h[1] = it.h[0] + 1;
-    it.q0[0] = it.q0[1] = row * kTile;
-  } else {
-    it.h[0] = it.h[1] = it.hk * a.G + p;
-    it.q0[0] = row * 2 * kTile;
-    it.q0[1] = it.q0[0] + kTile;
-  }
+  unsigned r = i / a.pairs;
+  const int p = static_cast<int>(i - r * a.pairs);
+  i = r / a.rows;
+  const int row = static_cast<int>(r - i * a.rows);
+  it.b = static_cast<int>(i / a.Hkv);
+  it.hk = static_cast<int>(i - it.b * a.Hkv);
+  it.h0 = it.hk * a.G + (a.by_head ? 2 * p : p);
+  it.dh = a.by_head ? 1 : 0;
+  it.q00 = row * (a.by_head ? kTile : 2 * kTile);
+  it.dq = a.by_head ? 0 : kTile;
   it.len = length_of(a.lens, it.b, a.N, &g_wfwd_status);
-  const int top = min(it.q0[1] + kTile, it.len) - 1;  // last query with keys
-  const int lo = max(0, it.q0[0] - a.window + 1);
+  const int top = min(it.q0(1) + kTile, it.len) - 1;  // last query with keys
+  const int lo = max(0, it.q00 - a.window + 1);
   it.first = lo / kTile;
   it.sink_steps = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
-  it.steps = it.q0[0] < it.len ? it.sink_steps + top / kTile - it.first + 1 : 0;
+  it.steps = it.q00 < it.len ? it.sink_steps + top / kTile - it.first + 1 : 0;
   return it;
 }
 
@@ -136,7 +134,7 @@ __device__ void load_role(const CUtensorMap* mq, const CUtensorMap* mk, const CU
   const int lane = threadIdx.x & 31;
   uint32_t n = 0, items = 0, fixes = 0;
   bool ok = true;
-  for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+  for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
     const Item it = item_of(a, i);
     if (it.steps == 0) continue;
     for (int s = 0; s < kSlots && ok; ++s) {
@@ -144,7 +142,7 @@ __device__ void load_role(const CUtensorMap* mq, const CUtensorMap* mk, const CU
       if (ok && lane == 0) {
         mbar_arrive_expect_tx(&ctl->q_full[s], C::TILE);
         for (int c = 0; c < C::ATOMS; ++c)
-          tma_load_4d(smem + s * C::TILE + c * kAtom, mq, &ctl->q_full[s], 64 * c, it.q0[s], it.h[s], it.b);
+          tma_load_4d(smem + s * C::TILE + c * kAtom, mq, &ctl->q_full[s], 64 * c, it.q0(s), it.h(s), it.b);
       }
     }
     ++items;
@@ -207,26 +205,25 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sbase, int s, i
   using C = Cfg<D>;
   constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
   const uint64_t bd = sdesc_sw128(sbase + C::OFF_KV + st * C::TILE, kAtom, 1024);
-  if (narrow) {
-    for (int kk = 0; kk < 2; ++kk)
-      umma_bf16_ts(tmem + C::TMEM_O + s * D, tmem + s * 128 + 8 * kk, bd + ((kk * 16 * 128) >> 4), kIdesc,
-                   (add || kk > 0) ? 1u : 0u);
-  } else {
-    umma_pv_chain8(tmem + C::TMEM_O + s * D, tmem + s * 128, static_cast<uint32_t>(bd),
-                   static_cast<uint32_t>(bd >> 32), kIdesc, add ? 1u : 0u);
-  }
+  const uint32_t lo = static_cast<uint32_t>(bd), hi = static_cast<uint32_t>(bd >> 32);
+  const uint32_t t_o = tmem + C::TMEM_O + s * D, t_p = tmem + s * 128;
+  if (narrow)
+    umma_pv_split2(t_o, t_p, lo, hi, kIdesc, add ? 1u : 0u);
+  else
+    umma_pv_split8(t_o, t_p, lo, hi, kIdesc, add ? 1u : 0u);
 }
 
+// The whole warp walks the steps, so that what the products need stays in uniform
+// registers; one lane issues them.
 template <int D>
 __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t tmem) {
   using C = Cfg<D>;
   const uint32_t sbase = smem_u32(smem);
+  const bool lead = elect_one();
   uint32_t n = 0, items = 0, p_seen = 0;  // tiles consumed, items begun, steps per slot
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return wait_bounded(bar, parity, &ctl->abort, &g_wfwd_status);
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl); };
   bool ok = true;
-  for (long long i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+  for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
     const Item it = item_of(a, i);
     if (it.steps == 0) continue;
     int kst = n % C::STAGES;
@@ -235,12 +232,14 @@ __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t 
       ok = wait(&ctl->q_full[s], items & 1);
       if (!ok) break;
       tc_fence_after();
-      issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, 0));
-      umma_commit(&ctl->s_full[s]);
-      if (it.steps == 1) umma_commit(&ctl->q_empty[s]);
+      if (lead) {
+        issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, 0));
+        umma_commit(&ctl->s_full[s]);
+        if (it.steps == 1) umma_commit(&ctl->q_empty[s]);
+      }
     }
     if (!ok) break;
-    umma_commit(&ctl->kv_empty[kst]);
+    if (lead) umma_commit(&ctl->kv_empty[kst]);
     ++n;
     for (int j = 0; j < it.steps && ok; ++j) {
       const int vst = n % C::STAGES;
@@ -250,25 +249,30 @@ __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t 
       kst = n % C::STAGES;
       const uint32_t kpar = (n / C::STAGES) & 1;
       if (more) ++n;
+      const bool narrow = narrow_step(a, it, j), next_narrow = narrow_step(a, it, j + 1);
+#pragma unroll
       for (int s = 0; s < kSlots; ++s) {
-        if (s == 0) ok = wait(&ctl->kv_full[vst], vpar);
+        if (s == 0) {
+          ok = wait(&ctl->kv_full[vst], vpar);
+          if (more) ok = ok && wait(&ctl->kv_full[kst], kpar);
+        }
         if (j == 0 && items > 0) ok = ok && wait(&ctl->o_free[s], (items - 1) & 1);
         ok = ok && wait(&ctl->p_full[s], p_seen & 1);
         if (!ok) break;
         tc_fence_after();
-        issue_pv<D>(tmem, sbase, s, vst, narrow_step(a, it, j), j > 0);
-        if (!more) umma_commit(&ctl->o_full[s]);
-        if (s == 1) umma_commit(&ctl->kv_empty[vst]);
-        if (more) {
-          if (s == 0) {
-            ok = wait(&ctl->kv_full[kst], kpar);
-            if (!ok) break;
-            tc_fence_after();
+        if (lead) {
+          issue_pv<D>(tmem, sbase, s, vst, narrow, j > 0);
+          if (more) {
+            issue_qk<D>(tmem, sbase, s, kst, next_narrow);
+            umma_commit(&ctl->s_full[s]);
+            if (j + 2 == it.steps) umma_commit(&ctl->q_empty[s]);
+          } else {
+            umma_commit(&ctl->o_full[s]);
           }
-          issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, j + 1));
-          umma_commit(&ctl->s_full[s]);
-          if (j + 2 == it.steps) umma_commit(&ctl->q_empty[s]);
-          if (s == 1) umma_commit(&ctl->kv_empty[kst]);
+          if (s == 1) {
+            umma_commit(&ctl->kv_empty[vst]);
+            if (more) umma_commit(&ctl->kv_empty[kst]);
+          }
         }
       }
       ++p_seen;
@@ -276,186 +280,258 @@ __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t 
     ++items;
   }
   // Every MMA issued must complete before TMEM is released.
-  umma_commit(&ctl->final_bar);
-  wait_drain(&ctl->final_bar, 0, &g_wfwd_status);
+  if (lead) {
+    umma_commit(&ctl->final_bar);
+    wait_drain(&ctl->final_bar, 0, &g_wfwd_status);
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------- softmax
-// One step of one query row: NC scores to NC / 2 columns of P.
-template <int D, int NC>
-__device__ __forceinline__ void softmax_step(uint32_t t_s, uint32_t t_o, float sl2, bool neg, bool masked,
-                                             int c_hi, int c_lo, int c_sink, bool have_o, float& m, float& l) {
-  constexpr float kNegInf = -INFINITY;
-  float x[NC];
-  if constexpr (NC == 128)
-    tmem_ld128_wait(t_s, x);
-  else
-    tmem_ld32f_wait(t_s, x);
-  if (neg) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) x[c] = -x[c];
+// Two threads share a query row, 64 of a step's 128 scores each.  They agree on
+// the running maximum at a barrier of the slot's 256 threads that also votes
+// whether any of them wants it raised: mostly none does, and the barrier is all
+// that the agreement costs.  A thread's 64 scores pass through 32 registers: the
+// right half for its maximum, the left half for its maximum and its P (which
+// lands on scores already taken), then the right half again for its P.  That keeps
+// a thread under 96 registers, and so four softmax warps on a scheduler.
+__device__ __forceinline__ bool slot_vote(int s, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(mine ? 1u : 0u), "r"(s + 1)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void slot_sync(int s) {
+  asm volatile("barrier.cta.sync.aligned %0, 256;" ::"r"(s + 1) : "memory");
+}
+
+// Which of 32 columns from c0 on a row sees: those up to hi, from lo on or below
+// sink.
+__device__ __forceinline__ uint32_t upto(int n) {  // the n lowest bits
+  return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+struct Seen {
+  int hi, lo, sink;
+  __device__ __forceinline__ uint32_t columns(int c0) const {
+    return upto(hi + 1 - c0) & (~upto(lo - c0) | upto(sink - c0));
   }
-  if (masked) {
+};
+
+// 32 scores of a row from column c0 on, for a positive scale.  The sign is
+// compiled in, and a step without hidden scores branches around their masks.
+template <bool NEG>
+__device__ __forceinline__ void load_scores(float (&x)[32], uint32_t t_s, int c0, bool full, const Seen& seen) {
+  tmem_ld32f_wait(t_s + c0, x);
+  if constexpr (NEG) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (c > c_hi || (c < c_lo && c >= c_sink)) x[c] = kNegInf;
+    for (int c = 0; c < 32; ++c) x[c] = -x[c];
   }
-  float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+  if (!full) {
+    const uint32_t w = seen.columns(c0);
 #pragma unroll
-  for (int c = 0; c < NC; c += 8) {
+    for (int c = 0; c < 32; ++c)
+      if (!(w & (1u << c))) x[c] = -INFINITY;
+  }
+}
+
+__device__ __forceinline__ float max_of(const float (&x)[32]) {
+  float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+  for (int c = 4; c < 28; c += 8) {
     m0 = max3f(m0, x[c], x[c + 1]);
     m1 = max3f(m1, x[c + 2], x[c + 3]);
     m2 = max3f(m2, x[c + 4], x[c + 5]);
     m3 = max3f(m3, x[c + 6], x[c + 7]);
   }
-  const float hm = max3f(fmaxf(m0, m1), m2, m3) * sl2;
-  const bool need = hm > m + kRescale;
-  if (__any_sync(0xffffffffu, need)) {
-    float f = 1.f;
-    if (need) {
-      f = m == kNegInf ? 1.f : ex2_approx(m - hm);
-      m = hm;
-    }
-    l *= f;
-    // this step's S is ready, so the P V of every step before has completed
-    if (have_o && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t w[32];
-        tmem_ld32_wait(t_o + c0, w);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
-        tmem_st32_wait(t_o + c0, w);
-      }
-    }
-  }
-  const float nm = m == kNegInf ? 0.f : -m;
-  float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
-#pragma unroll
-  for (int g = 0; g < NC; g += 32) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      float p0 = x[g + c], p1 = x[g + c + 1], p2 = x[g + c + 2], p3 = x[g + c + 3];
-      fma2(p0, p1, sl2, nm);
-      fma2(p2, p3, sl2, nm);
-      if (D == 128 && (c / 4) % 4 == 3) {  // this share of 2^x on the FMA pipe
-        exp2_poly2(p0, p1);
-        exp2_poly2(p2, p3);
-      } else {
-        p0 = ex2_approx(p0);
-        p1 = ex2_approx(p1);
-        p2 = ex2_approx(p2);
-        p3 = ex2_approx(p3);
-      }
-      acc2(sa, sb, p0, p1);
-      acc2(sc, sd, p2, p3);
-      pk[c / 2] = pack_bf16x2(p0, p1);
-      pk[c / 2 + 1] = pack_bf16x2(p2, p3);
-    }
-    tmem_st16(t_s + g / 2, pk);
-  }
-  l += (sa + sb) + (sc + sd);
+  m0 = max3f(m0, x[28], x[29]);
+  m1 = max3f(m1, x[30], x[31]);
+  return max3f(fmaxf(m0, m1), m2, m3);
 }
 
+// The row's running maximum takes this thread's hm and its partner's in, with O
+// and the sums brought to it, where it grows by more than the threshold.
 template <int D>
+__device__ __forceinline__ void raise_max(int s, float hm, float* mine, const float* other, uint32_t t_o,
+                                          bool have_o, float& m, float& l) {
+  if (!slot_vote(s, hm > m + kRescale)) return;
+  *mine = hm;
+  slot_sync(s);
+  hm = fmaxf(hm, *other);
+  float f = 1.f;
+  if (hm > m + kRescale) {
+    f = m == -INFINITY ? 1.f : ex2_approx(m - hm);
+    m = hm;
+  }
+  l *= f;
+  // this step's S is ready, so the P V of every step before has completed
+  if (have_o && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < D / 2; c0 += 8) {
+      uint32_t w[8];  // few registers: this is rare, and the scores are live across it
+      tmem_ld8_wait(t_o + c0, w);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+      tmem_st8_wait(t_o + c0, w);
+    }
+  }
+  slot_sync(s);  // the exchange may be written again
+}
+
+// P of 32 scores, to 16 columns from t_p on; their sum.
+template <int D>
+__device__ __forceinline__ float exponentials(const float (&x)[32], uint32_t t_p, float sl2, float nm) {
+  float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
+  uint32_t pk[16];
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    float p0 = x[c], p1 = x[c + 1], p2 = x[c + 2], p3 = x[c + 3];
+    fma2(p0, p1, sl2, nm);
+    fma2(p2, p3, sl2, nm);
+    if (D == 128 && (c / 4) % 8 == 7) {  // this share of 2^x on the FMA pipe
+      exp2_poly2(p0, p1);
+      exp2_poly2(p2, p3);
+    } else {
+      p0 = ex2_approx(p0);
+      p1 = ex2_approx(p1);
+      p2 = ex2_approx(p2);
+      p3 = ex2_approx(p3);
+    }
+    acc2(sa, sb, p0, p1);
+    acc2(sc, sd, p2, p3);
+    pk[c / 2] = pack_bf16x2(p0, p1);
+    pk[c / 2 + 1] = pack_bf16x2(p2, p3);
+  }
+  tmem_st16(t_p, pk);
+  return (sa + sb) + (sc + sd);
+}
+
+// What is left to do for a thread's half row once its item's last step is taken.
+struct Rest {
+  uint4* out;
+  float inv;      // 1 / sum; 0: a row past the sequence's end
+  bool pending, write;
+};
+
+template <int D>
+__device__ __forceinline__ void store_half_row(const Rest& r, uint32_t t_o, bool have_o) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D / 2; c0 += 16) {
+    uint32_t w[16];
+    if (have_o) {
+      tmem_ld16(t_o + c0, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 16; ++c) asm volatile("" : "+r"(w[c]));  // no use above the wait
+    }
+    if (!r.write) continue;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (have_o && r.inv > 0.f) {
+        x.x = pack_bf16x2(__uint_as_float(w[8 * v]) * r.inv, __uint_as_float(w[8 * v + 1]) * r.inv);
+        x.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * r.inv, __uint_as_float(w[8 * v + 3]) * r.inv);
+        x.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * r.inv, __uint_as_float(w[8 * v + 5]) * r.inv);
+        x.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * r.inv, __uint_as_float(w[8 * v + 7]) * r.inv);
+      }
+      r.out[c0 / 8 + v] = x;
+    }
+  }
+}
+
+template <int D, bool NEG>
 __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
   using C = Cfg<D>;
-  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) & 7, wq = warp & 3, half = warp >> 2, lane = threadIdx.x & 31;
   const int row = wq * 32 + lane;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-  const uint32_t t_s = t_lane + s * 128, t_o = t_lane + C::TMEM_O + s * D;
-  const bool neg = a.scale_log2 < 0.f;
+  const uint32_t t_s = t_lane + s * 128, t_o = t_lane + C::TMEM_O + s * D + half * (D / 2);
   const float sl2 = fabsf(a.scale_log2);
+  float* mine = &ctl->row[s][half][row];
+  const float* other = &ctl->row[s][half ^ 1][row];
   uint32_t seen = 0, items = 0;
-  for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+  Rest rest;
+  rest.pending = false;
+  // O of the item before: after its last P V, and before the next item's first
+  auto finish = [&]() {
+    if (!warp_wait(&ctl->o_full[s], (items - 1) & 1, ctl)) return false;
+    tc_fence_after();
+    store_half_row<D>(rest, t_o, true);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->o_free[s]);
+    rest.pending = false;
+    return true;
+  };
+  for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
     const Item it = item_of(a, i);
-    if (it.steps == 0) continue;
-    const int q = it.q0[s] + row;
-    float m = -INFINITY, l = 0.f;
+    const int q0 = it.q0(s), q = q0 + row;
+    float m = -INFINITY, l = 0.f;  // maximum (log2 units) of the row, sum of this thread's columns
     for (int j = 0; j < it.steps; ++j) {
       const int k0 = it.key0(j);
       // all keys of the tile are visible to all of its rows
-      const bool full = k0 + kTile - 1 <= it.q0[s] &&
-                        (k0 > it.q0[s] + kTile - 1 - a.window || k0 + kTile <= a.sinks);
+      const bool full = k0 + kTile - 1 <= q0 && (k0 > q0 + kTile - 1 - a.window || k0 + kTile <= a.sinks);
       if (!warp_wait(&ctl->s_full[s], seen & 1, ctl)) return;
       ++seen;
       tc_fence_after();
-      if (narrow_step(a, it, j))
-        softmax_step<D, 32>(t_s, t_o, sl2, neg, true, q - k0, q - a.window + 1 - k0, a.sinks - k0, j > 0, m, l);
-      else
-        softmax_step<D, 128>(t_s, t_o, sl2, neg, !full, q - k0, q - a.window + 1 - k0, a.sinks - k0, j > 0, m, l);
+      const Seen vis = {q - k0, q - a.window + 1 - k0, a.sinks - k0};
+      float x[32];
+      if (narrow_step(a, it, j)) {
+        float hm = -INFINITY;
+        if (half == 0) {
+          load_scores<NEG>(x, t_s, 0, false, vis);
+          hm = max_of(x) * sl2;
+        }
+        raise_max<D>(s, hm, mine, other, t_o, j > 0, m, l);
+        if (half == 0) l += exponentials<D>(x, t_s, sl2, m == -INFINITY ? 0.f : -m);
+      } else {
+        const int c0 = 64 * half;
+        load_scores<NEG>(x, t_s, c0 + 32, full, vis);
+        float hm = max_of(x);
+        load_scores<NEG>(x, t_s, c0, full, vis);
+        hm = fmaxf(hm, max_of(x)) * sl2;
+        raise_max<D>(s, hm, mine, other, t_o, j > 0, m, l);
+        const float nm = m == -INFINITY ? 0.f : -m;
+        l += exponentials<D>(x, t_s + c0, sl2, nm);
+        load_scores<NEG>(x, t_s, c0 + 32, full, vis);
+        l += exponentials<D>(x, t_s + c0 + 16, sl2, nm);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[s]);
+      // The last item's O is stored here: its last P V ran beside this softmax, and
+      // this step's P V is all that waits for it.
+      if (rest.pending && !finish()) return;
     }
-    if (items > 0 && !warp_wait(&ctl->ml_free[s], (items - 1) & 1, ctl)) return;
-    ctl->ml[s][row] = make_float2(m, l);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->ml_full[s]);
-    ++items;
+
+    if (it.steps > 0) {
+      *mine = l;
+      slot_sync(s);
+      // added in one order by both, so that they divide by the same sum
+      l = half == 0 ? l + *other : *other + l;
+      slot_sync(s);  // the exchange may be written again
+      ++items;
+    }
+    const bool live = q < it.len;
+    rest.inv = live ? 1.f / l : 0.f;
+    rest.write = q < a.N;
+    rest.out = reinterpret_cast<uint4*>(a.O + it.b * a.o_sb + it.h(s) * a.o_sh + static_cast<long long>(q) * a.o_sn +
+                                        half * (D / 2));
+    if (half == 0 && q < a.N)
+      a.LSE[(static_cast<long long>(it.b) * a.H + it.h(s)) * a.N + q] = live ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (it.steps > 0)
+      rest.pending = true;
+    else
+      store_half_row<D>(rest, t_o, false);
   }
+  if (rest.pending) finish();
 }
 
-// ------------------------------------------------------------------ epilogue
-template <int D>
-__device__ void epilogue_role(const Args& a, Ctl* ctl, uint32_t tmem) {
-  using C = Cfg<D>;
-  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int row = wq * 32 + lane;
-  const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-  uint32_t items = 0;
-  for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
-    const Item it = item_of(a, i);
-    for (int s = 0; s < kSlots; ++s) {
-      const int q = it.q0[s] + row;
-      float m = -INFINITY, l = 0.f;
-      if (it.steps > 0) {
-        if (!warp_wait(&ctl->ml_full[s], items & 1, ctl)) return;
-        const float2 ml = ctl->ml[s][row];
-        m = ml.x;
-        l = ml.y;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->ml_free[s]);
-        if (!warp_wait(&ctl->o_full[s], items & 1, ctl)) return;
-        tc_fence_after();
-      }
-      const bool live = q < it.len;
-      const float inv = 1.f / l;
-      uint4* out = reinterpret_cast<uint4*>(a.O + it.b * a.o_sb + it.h[s] * a.o_sh + static_cast<long long>(q) * a.o_sn);
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t w[32];
-        if (it.steps > 0) tmem_ld32_wait(t_lane + C::TMEM_O + s * D + c0, w);
-        if (q < a.N) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 r = make_uint4(0u, 0u, 0u, 0u);
-            if (live) {
-              r.x = pack_bf16x2(__uint_as_float(w[8 * v]) * inv, __uint_as_float(w[8 * v + 1]) * inv);
-              r.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * inv, __uint_as_float(w[8 * v + 3]) * inv);
-              r.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * inv, __uint_as_float(w[8 * v + 5]) * inv);
-              r.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * inv, __uint_as_float(w[8 * v + 7]) * inv);
-            }
-            out[c0 / 8 + v] = r;
-          }
-        }
-      }
-      if (it.steps > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->o_free[s]);
-      }
-      if (q < a.N)
-        a.LSE[(static_cast<long long>(it.b) * a.H + it.h[s]) * a.N + q] =
-            live ? (m + log2f(l)) * kLn2 : -INFINITY;
-    }
-    if (it.steps > 0) ++items;
-  }
-}
-
-template <int D>
+template <int D, bool NEG>
 __global__ void __launch_bounds__(kThreads, 1)
     window_forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                           const __grid_constant__ CUtensorMap mv, const Args a) {
@@ -472,11 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->q_full[s], 1);
       mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->s_full[s], 1);
-      mbar_init(&ctl->p_full[s], 4);
+      mbar_init(&ctl->p_full[s], 8);
       mbar_init(&ctl->o_full[s], 1);
-      mbar_init(&ctl->o_free[s], 4);
-      mbar_init(&ctl->ml_full[s], 4);
-      mbar_init(&ctl->ml_free[s], 4);
+      mbar_init(&ctl->o_free[s], 8);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
@@ -496,24 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
 
-  // 512 threads are launched with 128 registers: 256 x 192 + 128 x 80 + 128 x 48
-  if (warp < 8) {
-    regs_more<192>();
-    softmax_role<D>(warp >> 2, a, ctl, tmem);
-    __syncwarp();
-  } else if (warp < 12) {
-    regs_less<80>();
-    epilogue_role<D>(a, ctl, tmem);
-    __syncwarp();
-  } else {
-    regs_less<48>();
-    if (warp == kMmaWarp) {
-      if ((threadIdx.x & 31) == 0) mma_role<D>(a, smem, ctl, tmem);
-    } else if (warp == kLoadWarp) {
-      load_role<D>(&mq, &mk, &mv, a, smem, ctl);
-    }
-    __syncwarp();
+  if (warp < kSoftWarps) {
+    softmax_role<D, NEG>(warp >> 3, a, ctl, tmem);
+  } else if (warp == kMmaWarp) {
+    mma_role<D>(a, smem, ctl, __shfl_sync(0xffffffffu, tmem, 0));
+  } else if (warp == kLoadWarp) {
+    load_role<D>(&mq, &mk, &mv, a, smem, ctl);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -531,11 +595,11 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const Args& 
     return BSA_ERR_CUDA;
   const int smem = C::OFF_CTL + static_cast<int>(sizeof(Ctl));
   static_assert(C::OFF_CTL + sizeof(Ctl) <= 232448, "227 KB of shared memory");
-  const auto kernel = window_forward_kernel<D>;
+  const auto kernel = a.scale_log2 < 0.f ? window_forward_kernel<D, true> : window_forward_kernel<D, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return BSA_ERR_CUDA;
-  const long long sms = sm_count();
-  kernel<<<static_cast<unsigned>(a.items < sms ? a.items : sms), kThreads, smem, s>>>(mq, mk, mv, a);
+  const unsigned sms = static_cast<unsigned>(sm_count());
+  kernel<<<a.items < sms ? a.items : sms, kThreads, smem, s>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -576,7 +640,9 @@ extern "C" int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bs
   a.rows = a.by_head ? tiles : (tiles + 1) / 2;
   a.window = window < N ? window : N;
   a.sinks = sinks < N ? sinks : N;
-  a.items = static_cast<long long>(B) * Hkv * a.rows * a.pairs;
+  const long long items = static_cast<long long>(B) * Hkv * a.rows * a.pairs;
+  if (items >= (1LL << 31)) return BSA_ERR_UNSUPPORTED;
+  a.items = static_cast<unsigned>(items);
   // never 0: hidden scores are -inf times it, and must stay -inf
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;
