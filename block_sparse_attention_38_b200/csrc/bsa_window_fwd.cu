@@ -22,13 +22,12 @@
 // bf16 and O += P V takes P from there.  A slot's next S is issued behind its
 // P V, so the order of issue protects P.  TMEM: 2 x 128 columns of S, 2 x d of O.
 //
-// The walk is the sink tiles, then the window's tiles.  Only tiles that cross the
+// The walk is the window's tiles, then the sink tiles.  Only tiles that cross the
 // diagonal, the window's lower edge or the sequence's end pay for masks, and a
 // sink tile of up to 32 visible keys is taken with 32 columns instead of 128.
 //
 // Softmax: maxima on raw scores, lazy rescale of O (only when the maximum grows by
-// more than 2^8, so P <= 2^8), 2^x with the scale folded in, part of it by a
-// polynomial on the FMA pipe.  P is rounded to bf16 (2^-8 at most, like the
+// more than 2^20), 2^x with the scale folded in.  P is rounded to bf16 (2^-8 at most, like the
 // operands it meets); maxima, sums and O are fp32.
 //
 // Every wait is bounded.
@@ -43,7 +42,10 @@ constexpr int kSlots = 2;
 constexpr int kSoftWarps = 16;                 // 8 per slot: two per TMEM lane quadrant
 constexpr int kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kThreads = 18 * 32;
-constexpr float kRescale = 8.f;  // log2 units
+// Log2 units.  P is a floating-point number in every place that holds it, so it may
+// be as large as 2^20 without losing anything (sums stay below 2^20 N); what a raise
+// costs is a round trip of O.
+constexpr float kRescale = 20.f;
 
 __device__ unsigned int g_wfwd_status;
 
@@ -61,12 +63,12 @@ struct Cfg {
 struct Ctl {
   uint64_t q_full[kSlots], q_empty[kSlots];
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[kSlots], p_full[kSlots];
+  uint64_t s_full[kSlots], p_full[kSlots], p_half[kSlots];
   uint64_t o_full[kSlots], o_free[kSlots];
   uint64_t fix, final_bar;
   uint32_t tmem_base;
   volatile int abort;
-  float row[kSlots][2][kTile];  // exchange between the two threads of a row
+  float row[kSlots][2][kTile];  // exchange between the two threads of a row: maxima, sums
 };
 
 struct Args {
@@ -79,6 +81,7 @@ struct Args {
   unsigned pairs;     // items per tile row of a cached head (G even: G / 2; else G)
   unsigned rows;      // tile rows: q tiles (G even) or pairs of them
   int by_head;        // the two slots are two heads
+  int wide;           // O's rows are 32-byte aligned
   int window, sinks;
   unsigned items;
   float scale_log2;
@@ -87,11 +90,11 @@ struct Args {
 struct Item {
   int b, hk, len;
   int h0, dh, q00, dq;  // slot 0's head and first query, and how far slot 1's are on
-  int sink_steps, first, steps;
+  int near, first, steps;  // the window's tiles, then the sinks' (few keys: a low first maximum)
   __device__ __forceinline__ int h(int s) const { return h0 + s * dh; }
   __device__ __forceinline__ int q0(int s) const { return q00 + s * dq; }
   __device__ __forceinline__ int key0(int j) const {
-    return (j < sink_steps ? j : first + j - sink_steps) * kTile;
+    return (j < near ? first + j : j - near) * kTile;
   }
 };
 
@@ -111,14 +114,23 @@ __device__ __forceinline__ Item item_of(const Args& a, unsigned i) {
   const int top = min(it.q0(1) + kTile, it.len) - 1;  // last query with keys
   const int lo = max(0, it.q00 - a.window + 1);
   it.first = lo / kTile;
-  it.sink_steps = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
-  it.steps = it.q00 < it.len ? it.sink_steps + top / kTile - it.first + 1 : 0;
+  it.near = top / kTile - it.first + 1;
+  it.steps = it.q00 < it.len ? it.near + min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first) : 0;
   return it;
+}
+
+// The next item from i on (by the grid's stride) that has steps; false: none.
+__device__ __forceinline__ bool seek(const Args& a, unsigned& i, Item& it) {
+  for (; i < a.items; i += gridDim.x) {
+    it = item_of(a, i);
+    if (it.steps > 0) return true;
+  }
+  return false;
 }
 
 // Columns a step takes: 32 where a sink tile outside the window shows no more.
 __device__ __forceinline__ bool narrow_step(const Args& a, const Item& it, int j) {
-  return j < it.sink_steps && a.sinks - j * kTile <= 32;
+  return j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl) {
@@ -200,84 +212,115 @@ __device__ __forceinline__ void issue_qk(uint32_t tmem, uint32_t sbase, int s, i
                         static_cast<uint32_t>(bd), static_cast<uint32_t>(bd >> 32), idesc);
 }
 
-template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sbase, int s, int st, bool narrow, bool add) {
+// O += P V.  P comes in two parts, the first half of each thread's columns and the
+// second (narrow steps: one part of 32), so that the first product runs beside the
+// second part's exponentials.
+template <int D, int PART, bool NARROW>
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sbase, int s, int st, bool add) {
   using C = Cfg<D>;
   constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
   const uint64_t bd = sdesc_sw128(sbase + C::OFF_KV + st * C::TILE, kAtom, 1024);
   const uint32_t lo = static_cast<uint32_t>(bd), hi = static_cast<uint32_t>(bd >> 32);
   const uint32_t t_o = tmem + C::TMEM_O + s * D, t_p = tmem + s * 128;
-  if (narrow)
-    umma_pv_split2(t_o, t_p, lo, hi, kIdesc, add ? 1u : 0u);
-  else
-    umma_pv_split8(t_o, t_p, lo, hi, kIdesc, add ? 1u : 0u);
+  umma_pv_slices2(t_o, t_p + 16 * PART, lo + 256 * PART, hi, kIdesc, add ? 1u : 0u);
+  if (!NARROW) umma_pv_slices2(t_o, t_p + 64 + 16 * PART, lo + 512 + 256 * PART, hi, kIdesc, 1u);
+}
+
+// The MMA warp's counters: tiles consumed, items begun, steps taken.
+struct Issued {
+  uint32_t tiles, items, steps;
+};
+
+// One step of both slots: O += P V, and behind it the slot's next S, of this item
+// (LAST false) or of the next one (LAST; if it exists).  q_done: that S is the last
+// to read its Q.
+template <int D, bool LAST>
+__device__ __forceinline__ bool mma_step(uint32_t tmem, uint32_t sbase, Ctl* ctl, bool lead, Issued& n, bool first,
+                                         bool narrow, bool more, bool next_narrow, bool q_done) {
+  using C = Cfg<D>;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl); };
+  const int vst = n.tiles % C::STAGES;
+  const uint32_t vpar = (n.tiles / C::STAGES) & 1;
+  ++n.tiles;
+  const int kst = n.tiles % C::STAGES;
+  const uint32_t kpar = (n.tiles / C::STAGES) & 1;
+  if (!LAST || more) ++n.tiles;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    if (s == 0) {
+      if (!wait(&ctl->kv_full[vst], vpar)) return false;
+      if ((!LAST || more) && !wait(&ctl->kv_full[kst], kpar)) return false;
+    }
+    if (first && n.items > 0 && !wait(&ctl->o_free[s], (n.items - 1) & 1)) return false;
+    if (!narrow) {
+      if (!wait(&ctl->p_half[s], n.steps & 1)) return false;
+      tc_fence_after();
+      if (lead) issue_pv<D, 0, false>(tmem, sbase, s, vst, !first);
+    }
+    if (!wait(&ctl->p_full[s], n.steps & 1)) return false;
+    tc_fence_after();
+    if (lead) {
+      if (narrow)
+        issue_pv<D, 0, true>(tmem, sbase, s, vst, !first);
+      else
+        issue_pv<D, 1, false>(tmem, sbase, s, vst, true);
+    }
+    if (LAST) {
+      if (lead) umma_commit(&ctl->o_full[s]);
+      if (more && !wait(&ctl->q_full[s], (n.items + 1) & 1)) return false;
+      tc_fence_after();
+    }
+    if (lead) {
+      if (!LAST || more) {
+        issue_qk<D>(tmem, sbase, s, kst, next_narrow);
+        umma_commit(&ctl->s_full[s]);
+        if (q_done) umma_commit(&ctl->q_empty[s]);
+      }
+      if (s == 1) {
+        umma_commit(&ctl->kv_empty[vst]);
+        if (!LAST || more) umma_commit(&ctl->kv_empty[kst]);
+      }
+    }
+  }
+  ++n.steps;
+  return true;
 }
 
 // The whole warp walks the steps, so that what the products need stays in uniform
-// registers; one lane issues them.
+// registers; one lane issues them.  A slot's next S follows its P V at once, the
+// next item's first S too, so the slots stay half a step apart.
 template <int D>
 __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t tmem) {
-  using C = Cfg<D>;
   const uint32_t sbase = smem_u32(smem);
   const bool lead = elect_one();
-  uint32_t n = 0, items = 0, p_seen = 0;  // tiles consumed, items begun, steps per slot
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, ctl); };
-  bool ok = true;
-  for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
-    const Item it = item_of(a, i);
-    if (it.steps == 0) continue;
-    int kst = n % C::STAGES;
-    ok = wait(&ctl->kv_full[kst], (n / C::STAGES) & 1);
+  Issued n = {0, 0, 0};
+  unsigned i = blockIdx.x;
+  Item it;
+  bool have = seek(a, i, it), ok = true;
+  if (have) {
+    ok = warp_wait(&ctl->kv_full[0], 0, ctl);
     for (int s = 0; s < kSlots && ok; ++s) {
-      ok = wait(&ctl->q_full[s], items & 1);
-      if (!ok) break;
+      if (!(ok = warp_wait(&ctl->q_full[s], 0, ctl))) break;
       tc_fence_after();
       if (lead) {
-        issue_qk<D>(tmem, sbase, s, kst, narrow_step(a, it, 0));
+        issue_qk<D>(tmem, sbase, s, 0, narrow_step(a, it, 0));
         umma_commit(&ctl->s_full[s]);
         if (it.steps == 1) umma_commit(&ctl->q_empty[s]);
       }
     }
-    if (!ok) break;
-    if (lead) umma_commit(&ctl->kv_empty[kst]);
-    ++n;
-    for (int j = 0; j < it.steps && ok; ++j) {
-      const int vst = n % C::STAGES;
-      const uint32_t vpar = (n / C::STAGES) & 1;
-      ++n;
-      const bool more = j + 1 < it.steps;
-      kst = n % C::STAGES;
-      const uint32_t kpar = (n / C::STAGES) & 1;
-      if (more) ++n;
-      const bool narrow = narrow_step(a, it, j), next_narrow = narrow_step(a, it, j + 1);
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s) {
-        if (s == 0) {
-          ok = wait(&ctl->kv_full[vst], vpar);
-          if (more) ok = ok && wait(&ctl->kv_full[kst], kpar);
-        }
-        if (j == 0 && items > 0) ok = ok && wait(&ctl->o_free[s], (items - 1) & 1);
-        ok = ok && wait(&ctl->p_full[s], p_seen & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {
-          issue_pv<D>(tmem, sbase, s, vst, narrow, j > 0);
-          if (more) {
-            issue_qk<D>(tmem, sbase, s, kst, next_narrow);
-            umma_commit(&ctl->s_full[s]);
-            if (j + 2 == it.steps) umma_commit(&ctl->q_empty[s]);
-          } else {
-            umma_commit(&ctl->o_full[s]);
-          }
-          if (s == 1) {
-            umma_commit(&ctl->kv_empty[vst]);
-            if (more) umma_commit(&ctl->kv_empty[kst]);
-          }
-        }
-      }
-      ++p_seen;
-    }
-    ++items;
+    if (ok && lead) umma_commit(&ctl->kv_empty[0]);
+    n.tiles = 1;
+  }
+  while (have && ok) {
+    for (int j = 0; j + 1 < it.steps && ok; ++j)
+      ok = mma_step<D, false>(tmem, sbase, ctl, lead, n, j == 0, narrow_step(a, it, j), true,
+                              narrow_step(a, it, j + 1), j + 2 == it.steps);
+    const bool one = it.steps == 1, narrow = narrow_step(a, it, it.steps - 1);
+    i += gridDim.x;
+    have = seek(a, i, it);
+    ok = ok && mma_step<D, true>(tmem, sbase, ctl, lead, n, one, narrow, have, have && narrow_step(a, it, 0),
+                                 have && it.steps == 1);
+    ++n.items;
   }
   // Every MMA issued must complete before TMEM is released.
   if (lead) {
@@ -382,7 +425,6 @@ __device__ __forceinline__ void raise_max(int s, float hm, float* mine, const fl
 }
 
 // P of 32 scores, to 16 columns from t_p on; their sum.
-template <int D>
 __device__ __forceinline__ float exponentials(const float (&x)[32], uint32_t t_p, float sl2, float nm) {
   float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
   uint32_t pk[16];
@@ -391,15 +433,10 @@ __device__ __forceinline__ float exponentials(const float (&x)[32], uint32_t t_p
     float p0 = x[c], p1 = x[c + 1], p2 = x[c + 2], p3 = x[c + 3];
     fma2(p0, p1, sl2, nm);
     fma2(p2, p3, sl2, nm);
-    if (D == 128 && (c / 4) % 8 == 7) {  // this share of 2^x on the FMA pipe
-      exp2_poly2(p0, p1);
-      exp2_poly2(p2, p3);
-    } else {
-      p0 = ex2_approx(p0);
-      p1 = ex2_approx(p1);
-      p2 = ex2_approx(p2);
-      p3 = ex2_approx(p3);
-    }
+    p0 = ex2_approx(p0);
+    p1 = ex2_approx(p1);
+    p2 = ex2_approx(p2);
+    p3 = ex2_approx(p3);
     acc2(sa, sb, p0, p1);
     acc2(sc, sd, p2, p3);
     pk[c / 2] = pack_bf16x2(p0, p1);
@@ -411,33 +448,33 @@ __device__ __forceinline__ float exponentials(const float (&x)[32], uint32_t t_p
 
 // What is left to do for a thread's half row once its item's last step is taken.
 struct Rest {
-  uint4* out;
-  float inv;      // 1 / sum; 0: a row past the sequence's end
-  bool pending, write;
+  __nv_bfloat16* out;
+  float* lse;
+  float m, l;
+  bool pending, live, write;   // live: a row of the sequence; write: a row of the tensor
 };
 
+// A half row of O / sum, 32 bytes at a time where the rows are aligned so.
 template <int D>
-__device__ __forceinline__ void store_half_row(const Rest& r, uint32_t t_o, bool have_o) {
+__device__ __forceinline__ void store_half_row(const Rest& r, float inv, uint32_t t_o, bool have_o, bool wide) {
 #pragma unroll 1
   for (int c0 = 0; c0 < D / 2; c0 += 16) {
-    uint32_t w[16];
+    uint32_t w[16], x[8];
     if (have_o) {
       tmem_ld16(t_o + c0, w);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 16; ++c) asm volatile("" : "+r"(w[c]));  // no use above the wait
     }
-    if (!r.write) continue;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (have_o && r.inv > 0.f) {
-        x.x = pack_bf16x2(__uint_as_float(w[8 * v]) * r.inv, __uint_as_float(w[8 * v + 1]) * r.inv);
-        x.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * r.inv, __uint_as_float(w[8 * v + 3]) * r.inv);
-        x.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * r.inv, __uint_as_float(w[8 * v + 5]) * r.inv);
-        x.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * r.inv, __uint_as_float(w[8 * v + 7]) * r.inv);
-      }
-      r.out[c0 / 8 + v] = x;
+    for (int c = 0; c < 8; ++c)
+      x[c] = have_o && r.live ? pack_bf16x2(__uint_as_float(w[2 * c]) * inv, __uint_as_float(w[2 * c + 1]) * inv) : 0u;
+    if (!r.write) continue;
+    if (wide) {
+      store_256(r.out + c0, x);
+    } else {
+      *reinterpret_cast<uint4*>(r.out + c0) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(r.out + c0 + 8) = make_uint4(x[4], x[5], x[6], x[7]);
     }
   }
 }
@@ -455,14 +492,21 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
   uint32_t seen = 0, items = 0;
   Rest rest;
   rest.pending = false;
-  // O of the item before: after its last P V, and before the next item's first
+  // O of the item before: after its last P V, and before the next item's first.
+  // The exchange is free again after the next step's vote, before which nothing
+  // writes it.
   auto finish = [&]() {
+    *mine = rest.l;
+    slot_sync(s);
+    // added in one order by both, so that they divide by the same sum
+    const float l = half == 0 ? rest.l + *other : *other + rest.l;
     if (!warp_wait(&ctl->o_full[s], (items - 1) & 1, ctl)) return false;
     tc_fence_after();
-    store_half_row<D>(rest, t_o, true);
+    store_half_row<D>(rest, 1.f / l, t_o, true, a.wide);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->o_free[s]);
+    if (half == 0 && rest.write) *rest.lse = rest.live ? (rest.m + log2f(l)) * kLn2 : -INFINITY;
     rest.pending = false;
     return true;
   };
@@ -486,7 +530,8 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
           hm = max_of(x) * sl2;
         }
         raise_max<D>(s, hm, mine, other, t_o, j > 0, m, l);
-        if (half == 0) l += exponentials<D>(x, t_s, sl2, m == -INFINITY ? 0.f : -m);
+        if (half == 0) l += exponentials(x, t_s, sl2, m == -INFINITY ? 0.f : -m);
+        if (lane == 0) mbar_arrive(&ctl->p_half[s]);
       } else {
         const int c0 = 64 * half;
         load_scores<NEG>(x, t_s, c0 + 32, full, vis);
@@ -495,9 +540,13 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
         hm = fmaxf(hm, max_of(x)) * sl2;
         raise_max<D>(s, hm, mine, other, t_o, j > 0, m, l);
         const float nm = m == -INFINITY ? 0.f : -m;
-        l += exponentials<D>(x, t_s + c0, sl2, nm);
+        l += exponentials(x, t_s + c0, sl2, nm);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_half[s]);
         load_scores<NEG>(x, t_s, c0 + 32, full, vis);
-        l += exponentials<D>(x, t_s + c0 + 16, sl2, nm);
+        l += exponentials(x, t_s + c0 + 16, sl2, nm);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -508,25 +557,19 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
       if (rest.pending && !finish()) return;
     }
 
-    if (it.steps > 0) {
-      *mine = l;
-      slot_sync(s);
-      // added in one order by both, so that they divide by the same sum
-      l = half == 0 ? l + *other : *other + l;
-      slot_sync(s);  // the exchange may be written again
-      ++items;
-    }
-    const bool live = q < it.len;
-    rest.inv = live ? 1.f / l : 0.f;
+    rest.out = a.O + it.b * a.o_sb + it.h(s) * a.o_sh + static_cast<long long>(q) * a.o_sn + half * (D / 2);
+    rest.lse = a.LSE + (static_cast<long long>(it.b) * a.H + it.h(s)) * a.N + q;
+    rest.m = m;
+    rest.l = l;
+    rest.live = q < it.len;
     rest.write = q < a.N;
-    rest.out = reinterpret_cast<uint4*>(a.O + it.b * a.o_sb + it.h(s) * a.o_sh + static_cast<long long>(q) * a.o_sn +
-                                        half * (D / 2));
-    if (half == 0 && q < a.N)
-      a.LSE[(static_cast<long long>(it.b) * a.H + it.h(s)) * a.N + q] = live ? (m + log2f(l)) * kLn2 : -INFINITY;
-    if (it.steps > 0)
+    if (it.steps > 0) {
       rest.pending = true;
-    else
-      store_half_row<D>(rest, t_o, false);
+      ++items;
+    } else {
+      store_half_row<D>(rest, 0.f, t_o, false, a.wide);
+      if (half == 0 && rest.write) *rest.lse = -INFINITY;
+    }
   }
   if (rest.pending) finish();
 }
@@ -549,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->s_full[s], 1);
       mbar_init(&ctl->p_full[s], 8);
+      mbar_init(&ctl->p_half[s], 8);
       mbar_init(&ctl->o_full[s], 1);
       mbar_init(&ctl->o_free[s], 8);
     }
@@ -628,6 +672,7 @@ extern "C" int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bs
   a.o_sb = B > 1 ? o->stride_b : 0;
   a.o_sh = H > 1 ? o->stride_h : 0;
   a.o_sn = N > 1 ? o->stride_n : 0;
+  a.wide = (reinterpret_cast<uintptr_t>(o->data) & 31u) == 0 && ((a.o_sb | a.o_sh | a.o_sn) & 15) == 0;
   a.LSE = LSE;
   a.B = B;
   a.H = H;

@@ -374,35 +374,8 @@ __device__ __forceinline__ void umma_pv_chain8(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
-// The same product with A in two pieces: columns 0 .. 31 hold entries 0 .. 63 of the
-// summed index, columns 64 .. 95 the rest; and its first two slices alone (32
-// entries).
-__device__ __forceinline__ void umma_pv_split8(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                               uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p0, pt;\n\t.reg .b32 bl, at, one;\n\t.reg .b64 bd;\n\t"
-      "mov.b32 one, 1;\n\tsetp.eq.b32 pt, one, 1;\n\tsetp.ne.b32 p0, %5, 0;\n\t"
-      "add.s32 at, %1, 0;\n\tadd.s32 bl, %2, 0;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, p0;\n\t"
-      "add.s32 at, %1, 8;\n\tadd.s32 bl, %2, 128;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 16;\n\tadd.s32 bl, %2, 256;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 24;\n\tadd.s32 bl, %2, 384;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 64;\n\tadd.s32 bl, %2, 512;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 72;\n\tadd.s32 bl, %2, 640;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 80;\n\tadd.s32 bl, %2, 768;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "add.s32 at, %1, 88;\n\tadd.s32 bl, %2, 896;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "}"
-      :: "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_pv_split2(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+// Two K=16 slices of the same product.
+__device__ __forceinline__ void umma_pv_slices2(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                                uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p0, pt;\n\t.reg .b32 bl, at, one;\n\t.reg .b64 bd;\n\t"
@@ -496,6 +469,13 @@ __device__ __forceinline__ void regs_less() {
 // proxy (tcgen05.mma, TMA stores).
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 32 bytes to a 32-byte aligned address: one full sector a lane.
+__device__ __forceinline__ void store_256(void* dst, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // ------------------------------------------------------------------- math
