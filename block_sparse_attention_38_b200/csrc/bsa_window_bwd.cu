@@ -49,11 +49,13 @@ struct Args {
   __nv_bfloat16* out[2];     // dV, dK, or dQ
   long long sb[2], sh[2], sn[2];
   float* part;               // [B * Hkv, sink tiles, 1 + chunks, 2, 128, d]
-  int B, H, Hkv, G, N, tiles;
+  int B, H, N;
+  unsigned Hkv, G, tiles;
   int window, sinks;
-  int sink_tiles;            // key tiles with sinks that have far queries
-  int chunks, chunk_tiles;   // far chunks per sink tile, query tiles in each
-  long long items;
+  unsigned sink_tiles;       // key tiles with sinks that have far queries
+  unsigned chunks;           // far chunks per sink tile, of chunk_tiles query tiles
+  int chunk_tiles;
+  unsigned items;
   float scale, scale_log2;
 };
 
@@ -84,15 +86,18 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_smem, uint32_
 }
 
 // C (+)= A B with A in TMEM (bf16 pairs; columns 64 h .. 64 h + 31 hold entries
-// 64 h .. 64 h + 63 of the summed index) and B a tile read MN-major.
+// 64 h .. 64 h + 63 of the summed index) and B a tile read MN-major.  narrow: the
+// first 32 entries only.
 template <int D>
-__device__ __forceinline__ void mma_ts(uint32_t c_tmem, uint32_t a_tmem, uint32_t b_smem, int slices, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t c_tmem, uint32_t a_tmem, uint32_t b_smem, bool narrow, bool add) {
   constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
   const uint64_t bd = sdesc_sw128(b_smem, kAtom, 1024);
-#pragma unroll 8
-  for (int kk = 0; kk < slices; ++kk)
-    umma_bf16_ts(c_tmem, a_tmem + (kk >> 2) * 64 + (kk & 3) * 8, bd + ((kk * 16 * 128) >> 4), kIdesc,
-                 (add || kk > 0) ? 1u : 0u);
+  const uint32_t lo = static_cast<uint32_t>(bd), hi = static_cast<uint32_t>(bd >> 32);
+  umma_pv_slices2(c_tmem, a_tmem, lo, hi, kIdesc, add ? 1u : 0u);
+  if (narrow) return;
+  umma_pv_slices2(c_tmem, a_tmem + 16, lo + 256, hi, kIdesc, 1u);
+  umma_pv_slices2(c_tmem, a_tmem + 64, lo + 512, hi, kIdesc, 1u);
+  umma_pv_slices2(c_tmem, a_tmem + 80, lo + 768, hi, kIdesc, 1u);
 }
 
 // 2^x of 32 scaled scores: every fourth group of four on the FMA pipe.
@@ -173,23 +178,23 @@ struct KvItem {
   int first, count;                  // query tiles
 };
 
-__device__ __forceinline__ KvItem kv_item(const Args& a, long long i) {
+__device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
   KvItem it;
-  const long long main_items = static_cast<long long>(a.B) * a.Hkv * a.tiles;
-  long long bh;
+  const unsigned main_items = static_cast<unsigned>(a.B) * a.Hkv * a.tiles;
+  unsigned bh;
   int chunk = -1;
   if (i < main_items) {
-    it.kt = static_cast<int>(i % a.tiles);
     bh = i / a.tiles;
+    it.kt = static_cast<int>(i - bh * a.tiles);
   } else {
     i -= main_items;
-    chunk = static_cast<int>(i % a.chunks);
-    i /= a.chunks;
-    it.kt = static_cast<int>(i % a.sink_tiles);
-    bh = i / a.sink_tiles;
+    unsigned r = i / a.chunks;
+    chunk = static_cast<int>(i - r * a.chunks);
+    bh = r / a.sink_tiles;
+    it.kt = static_cast<int>(r - bh * a.sink_tiles);
   }
   it.b = static_cast<int>(bh / a.Hkv);
-  it.hk = static_cast<int>(bh % a.Hkv);
+  it.hk = static_cast<int>(bh - it.b * a.Hkv);
   it.k0 = it.kt * kTile;
   it.len = length_of(a.lens, it.b, a.N, &g_wbwd_status);
   const int last = (it.len - 1) / kTile;                       // last query tile with queries
@@ -199,7 +204,7 @@ __device__ __forceinline__ KvItem kv_item(const Args& a, long long i) {
   if (chunk < 0) {
     it.first = it.kt;
     end = min(near, last);
-    it.slot = it.kt < a.sink_tiles ? 0 : -1;
+    it.slot = it.kt < static_cast<int>(a.sink_tiles) ? 0 : -1;
   } else {
     it.first = near + 1 + chunk * a.chunk_tiles;
     end = min(it.first + a.chunk_tiles - 1, last);
@@ -225,12 +230,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   KvCtl* ctl = reinterpret_cast<KvCtl*>(smem + 6 * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvItem it = kv_item(a, blockIdx.x);
-  const int steps = it.count * a.G;
+  const int G = static_cast<int>(a.G), steps = it.count * G;
 
   if (tid == 0) {
     mbar_init(&ctl->kv_full, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl->q_full[s], 1);
+      mbar_init(&ctl->q_full[s], 2);
       mbar_init(&ctl->q_empty[s], 1);
       mbar_init(&ctl->do_full[s], 1);
       mbar_init(&ctl->do_empty[s], 1);
@@ -267,28 +272,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(sV + c * kAtom, &mv, &ctl->kv_full, 64 * c, it.k0, it.hk, it.b);
       }
     }
+    // LSE and D of a step's queries, loaded a step ahead: four of each a lane
+    float lse[4], dd[4];
+    auto fetch = [&](int j) {
+      const int qt = j / G;
+      const long long row = (static_cast<long long>(it.b) * a.H + it.hk * G + j - qt * G) * a.N;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int q = (it.first + qt) * kTile + r * 32 + lane;
+        lse[r] = j < steps && q < a.N ? a.LSE[row + q] : 0.f;
+        dd[r] = j < steps && q < a.N ? a.Dq[row + q] : 0.f;
+      }
+    };
+    fetch(0);
     int issued = 0;
     for (int j = 0; j < steps && ok; ++j) {
-      const int s = j & 1, q0 = (it.first + j / a.G) * kTile, h = it.hk * a.G + j % a.G;
+      const int s = j & 1, qt = j / G, q0 = (it.first + qt) * kTile, h = it.hk * G + j - qt * G;
       const bool fix = q0 + kTile > it.len && it.len < a.N;
       for (int w = 0; w < 2 && ok; ++w) {
         unsigned char* dst = (w == 0 ? sQ : sO) + s * C::TILE;
         uint64_t* full = w == 0 ? &ctl->q_full[s] : &ctl->do_full[s];
         if (j >= 2) ok = __all_sync(0xffffffffu, wait(w == 0 ? &ctl->q_empty[s] : &ctl->do_empty[s], ((j >> 1) - 1) & 1));
         if (!ok) break;
-        if (w == 0) {
-          const long long row = (static_cast<long long>(it.b) * a.H + h) * a.N;
-          for (int r = lane; r < kTile; r += 32) {
-            const int q = q0 + r;
-            ctl->lse2[s][r] = q < a.N ? a.LSE[row + q] * kLog2e : 0.f;
-            ctl->dq[s][r] = q < a.N ? a.Dq[row + q] : 0.f;
-          }
-          __syncwarp();
-        }
         uint64_t* bar = fix ? &ctl->fix : full;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, C::TILE);
           for (int c = 0; c < C::ATOMS; ++c) tma_load_4d(dst + c * kAtom, w == 0 ? &mq : &mo, bar, 64 * c, q0, h, it.b);
+        }
+        if (w == 0) {  // q_full takes a second arrival, for these
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            ctl->lse2[s][r * 32 + lane] = lse[r] * kLog2e;
+            ctl->dq[s][r * 32 + lane] = dd[r];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+          fetch(j + 1);
         }
         if (fix) {
           ok = __all_sync(0xffffffffu, wait(&ctl->fix, fixes & 1));
@@ -310,38 +329,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       if (fixes > 0) wait_drain(&ctl->fix, (fixes - 1) & 1, &g_wbwd_status);
     }
-  } else if (warp == kMmaWarp && lane == 0) {
+  } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issuer
+    // The whole warp walks the steps, so that what the products need stays in
+    // uniform registers; one lane issues them.
     const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), o = smem_u32(sO);
-    bool ok = steps > 0 && wait(&ctl->kv_full, 0) && wait(&ctl->q_full[0], 0);
-    if (ok) {
+    const uint32_t t = __shfl_sync(0xffffffffu, tmem, 0);
+    const bool lead = elect_one();
+    auto arrived = [&](uint64_t* bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, wait(bar, parity))) return false;
       tc_fence_after();
-      mma_ss<D>(tmem + T_S, k, q, kIdesc);
+      return true;
+    };
+    bool ok = steps > 0 && arrived(&ctl->kv_full, 0) && arrived(&ctl->q_full[0], 0);
+    if (ok && lead) {
+      mma_ss<D>(t + T_S, k, q, kIdesc);
       umma_commit(&ctl->s_full);
     }
     for (int j = 0; j < steps && ok; ++j) {
       const int s = j & 1;
-      if (!(ok = wait(&ctl->do_full[s], (j >> 1) & 1))) break;
-      tc_fence_after();
-      mma_ss<D>(tmem + T_DP, v, o + s * C::TILE, kIdesc);
-      umma_commit(&ctl->dp_full);
-      if (!(ok = wait(&ctl->p_ready, j & 1))) break;
-      tc_fence_after();
-      mma_ts<D>(tmem + T_DV, tmem + T_S, o + s * C::TILE, 8, j > 0);
-      umma_commit(&ctl->do_empty[s]);
-      if (j + 1 < steps) {
-        if (!(ok = wait(&ctl->q_full[s ^ 1], ((j + 1) >> 1) & 1))) break;
-        tc_fence_after();
-        mma_ss<D>(tmem + T_S, k, q + (s ^ 1) * C::TILE, kIdesc);
-        umma_commit(&ctl->s_full);
+      const uint32_t qs = q + s * C::TILE, qn = q + (s ^ 1) * C::TILE, os = o + s * C::TILE;
+      if (!(ok = arrived(&ctl->do_full[s], (j >> 1) & 1))) break;
+      if (lead) {
+        mma_ss<D>(t + T_DP, v, os, kIdesc);
+        umma_commit(&ctl->dp_full);
       }
-      if (!(ok = wait(&ctl->ds_ready, j & 1))) break;
-      tc_fence_after();
-      mma_ts<D>(tmem + T_DK, tmem + T_DP, q + s * C::TILE, 8, j > 0);
-      umma_commit(&ctl->q_empty[s]);
+      if (j + 1 < steps && !(ok = arrived(&ctl->q_full[s ^ 1], ((j + 1) >> 1) & 1))) break;
+      if (!(ok = arrived(&ctl->p_ready, j & 1))) break;
+      if (lead) {
+        mma_ts<D>(t + T_DV, t + T_S, os, false, j > 0);
+        umma_commit(&ctl->do_empty[s]);
+        if (j + 1 < steps) {
+          mma_ss<D>(t + T_S, k, qn, kIdesc);
+          umma_commit(&ctl->s_full);
+        }
+      }
+      if (!(ok = arrived(&ctl->ds_ready, j & 1))) break;
+      if (lead) {
+        mma_ts<D>(t + T_DK, t + T_DP, qs, false, j > 0);
+        umma_commit(&ctl->q_empty[s]);
+      }
     }
-    umma_commit(&ctl->acc_full);  // every MMA issued must complete before TMEM is released
-    wait_drain(&ctl->acc_full, 0, &g_wbwd_status);
+    if (lead) {
+      umma_commit(&ctl->acc_full);  // every MMA issued must complete before TMEM is released
+      wait_drain(&ctl->acc_full, 0, &g_wbwd_status);
+    }
+    __syncwarp();
   } else if (warp < 8) {
     // ---------------------------------------------------------- elementwise
     const int quad = warp & 3, half = warp >> 2;
@@ -353,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool sink = k < a.sinks;
     bool ok = true;
     for (int j = 0; j < steps && ok; ++j) {
-      const int s = j & 1, q0 = (it.first + j / a.G) * kTile;
+      const int s = j & 1, q0 = (it.first + j / G) * kTile;
       float p[64];
       // q_full too: it orders the producer's writes of lse2 and dq before their reads
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full, j & 1) && wait(&ctl->q_full[s], (j >> 1) & 1));
@@ -475,7 +508,7 @@ __global__ void __launch_bounds__(256) sink_kernel(const Args a) {
   const int kt = static_cast<int>(tile % a.sink_tiles), k = kt * kTile + row;
   if (k >= a.N) return;
   const long long bh = tile / a.sink_tiles;
-  const int n = k < a.sinks ? 1 + a.chunks : 1;
+  const int n = k < a.sinks ? 1 + static_cast<int>(a.chunks) : 1;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < n; ++i) {
     const float4 x = *reinterpret_cast<const float4*>(
@@ -502,31 +535,31 @@ struct QCtl {
 
 struct QItem {
   int b, h, hk, q0, len;
-  int sink_steps, first, steps;
+  int near, first, steps;  // the window's tiles, then the sinks'
   __device__ __forceinline__ int key0(int j) const {
-    return (j < sink_steps ? j : first + j - sink_steps) * kTile;
+    return (j < near ? first + j : j - near) * kTile;
   }
 };
 
-__device__ __forceinline__ QItem q_item(const Args& a, long long i) {
+__device__ __forceinline__ QItem q_item(const Args& a, unsigned i) {
   QItem it;
-  const int g = static_cast<int>(i % a.G);
-  long long r = i / a.G;
-  it.q0 = static_cast<int>(r % a.tiles) * kTile;
-  r /= a.tiles;
-  it.hk = static_cast<int>(r % a.Hkv);
-  it.b = static_cast<int>(r / a.Hkv);
+  unsigned r = i / a.G;
+  const int g = static_cast<int>(i - r * a.G);
+  i = r / a.tiles;
+  it.q0 = static_cast<int>(r - i * a.tiles) * kTile;
+  it.b = static_cast<int>(i / a.Hkv);
+  it.hk = static_cast<int>(i - it.b * a.Hkv);
   it.h = it.hk * a.G + g;
   it.len = length_of(a.lens, it.b, a.N, &g_wbwd_status);
   it.first = max(0, it.q0 - a.window + 1) / kTile;
-  it.sink_steps = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
-  it.steps = it.q0 < it.len ? it.sink_steps + (min(it.q0 + kTile, it.len) - 1) / kTile - it.first + 1 : 0;
+  it.near = (min(it.q0 + kTile, it.len) - 1) / kTile - it.first + 1;
+  it.steps = it.q0 < it.len ? it.near + min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first) : 0;
   return it;
 }
 
 // Steps of this CTA's items, one after another.
 struct QWalk {
-  long long i;
+  unsigned i;
   QItem it;
   int j, n;          // step of the item, and the item's number among those with steps
   bool valid;
@@ -554,7 +587,7 @@ struct QWalk {
   __device__ __forceinline__ bool last() const { return j + 1 == it.steps; }
   // a sink tile outside the window that shows at most 32 keys takes 32 columns
   __device__ __forceinline__ bool narrow(const Args& a) const {
-    return j < it.sink_steps && a.sinks - j * kTile <= 32;
+    return j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
   }
 };
 
@@ -672,55 +705,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (items > 0) wait_drain(&ctl->do_full, (items - 1) & 1, &g_wbwd_status);
       if (fixes > 0) wait_drain(&ctl->fix, (fixes - 1) & 1, &g_wbwd_status);
     }
-  } else if (warp == kMmaWarp && lane == 0) {
+  } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issuer
     const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), o = smem_u32(sO);
-    auto idesc = [&](bool narrow) {
-      return narrow ? idesc_bf16_f32(128, 32, false, false) : idesc_bf16_f32(128, 128, false, false);
-    };
-    auto scores = [&](const QWalk& w, uint32_t t) {  // S of step t, the step w stands at
-      if (w.j == 0 && !wait(&ctl->q_full[w.n & 1], (w.n >> 1) & 1)) return false;
-      if (t > 0 && !wait(&ctl->s_free, (t - 1) & 1)) return false;
-      if (!wait(&ctl->k_full[t & 1], (t >> 1) & 1)) return false;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const bool lead = elect_one();
+    constexpr uint32_t kWide = idesc_bf16_f32(128, 128, false, false), kNarrow = idesc_bf16_f32(128, 32, false, false);
+    auto arrived = [&](uint64_t* bar, uint32_t parity) {
+      if (!warp_wait(bar, parity)) return false;
       tc_fence_after();
-      mma_ss<D>(tmem + T_S, q + (w.n & 1) * C::TILE, k + (t & 1) * C::TILE, idesc(w.narrow(a)));
-      umma_commit(&ctl->s_full);
-      if (w.last()) umma_commit(&ctl->q_empty[w.n & 1]);
+      return true;
+    };
+    // S of step t, the j-th of the n-th item
+    auto scores = [&](uint32_t t, int n, bool first, bool narrow, bool last) {
+      if (first && !arrived(&ctl->q_full[n & 1], (n >> 1) & 1)) return false;
+      if (t > 0 && !arrived(&ctl->s_free, (t - 1) & 1)) return false;
+      if (!arrived(&ctl->k_full[t & 1], (t >> 1) & 1)) return false;
+      if (lead) {
+        mma_ss<D>(tm + T_S, q + (n & 1) * C::TILE, k + (t & 1) * C::TILE, narrow ? kNarrow : kWide);
+        umma_commit(&ctl->s_full);
+        if (last) umma_commit(&ctl->q_empty[n & 1]);
+      }
+      return true;
+    };
+    // One step, with the next one's S before its dS is waited for.
+    auto step = [&](uint32_t t, int n, bool first, bool narrow, bool last, bool more, int nn, bool nfirst,
+                    bool nnarrow, bool nlast) {
+      const int s = t & 1, buf = n & 1;
+      if (first && !arrived(&ctl->do_full, n & 1)) return false;
+      if (!arrived(&ctl->v_full[s], (t >> 1) & 1)) return false;
+      if (lead) {
+        mma_ss<D>(tm + T_DP, o, v + s * C::TILE, narrow ? kNarrow : kWide);
+        umma_commit(&ctl->dp_full);
+        umma_commit(&ctl->v_empty[s]);
+        if (last) umma_commit(&ctl->do_empty);
+      }
+      if (more && !scores(t + 1, nn, nfirst, nnarrow, nlast)) return false;
+      if (first && n >= 2 && !arrived(&ctl->dq_free[buf], ((n >> 1) - 1) & 1)) return false;
+      if (!arrived(&ctl->ds_ready, t & 1)) return false;
+      if (lead) {
+        mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP, k + s * C::TILE, narrow, !first);
+        umma_commit(&ctl->k_empty[s]);
+        if (last) umma_commit(&ctl->dq_full[buf]);
+      }
       return true;
     };
     QWalk w;
     w.begin(a);
-    bool ok = !w.valid || scores(w, 0);
-    for (uint32_t t = 0; w.valid && ok; ++t) {
-      const int s = t & 1;
-      ok = (w.j > 0 || wait(&ctl->do_full, w.n & 1)) && wait(&ctl->v_full[s], (t >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      mma_ss<D>(tmem + T_DP, o, v + s * C::TILE, idesc(w.narrow(a)));
-      umma_commit(&ctl->dp_full);
-      umma_commit(&ctl->v_empty[s]);
-      if (w.last()) umma_commit(&ctl->do_empty);
-      QWalk nx = w;
-      nx.next(a);
-      if (nx.valid && !(ok = scores(nx, t + 1))) break;
-      const int buf = w.n & 1;
-      if (w.j == 0 && w.n >= 2 && !(ok = wait(&ctl->dq_free[buf], ((w.n >> 1) - 1) & 1))) break;
-      if (!(ok = wait(&ctl->ds_ready, t & 1))) break;
-      tc_fence_after();
-      mma_ts<D>(tmem + T_DQ + buf * D, tmem + T_DP, k + s * C::TILE, w.narrow(a) ? 2 : 8, w.j > 0);
-      umma_commit(&ctl->k_empty[s]);
-      if (w.last()) umma_commit(&ctl->dq_full[buf]);
-      w = nx;
+    bool ok = !w.valid || scores(0, 0, true, w.narrow(a), w.last());
+    uint32_t t = 0;
+    while (w.valid && ok) {
+      const int n = w.n, steps = w.it.steps;
+      for (; w.j + 1 < steps && ok; ++w.j, ++t) {
+        const bool narrow = w.narrow(a), first = w.j == 0;
+        QWalk nx = w;
+        ++nx.j;
+        ok = step(t, n, first, narrow, false, true, n, false, nx.narrow(a), nx.j + 1 == steps);
+      }
+      const bool one = steps == 1, narrow = w.narrow(a);
+      w.next(a);
+      ok = ok && step(t, n, one, narrow, true, w.valid, n + 1, true, w.valid && w.narrow(a), w.valid && w.last());
+      ++t;
     }
-    umma_commit(&ctl->final_bar);
-    wait_drain(&ctl->final_bar, 0, &g_wbwd_status);
+    if (lead) {
+      umma_commit(&ctl->final_bar);
+      wait_drain(&ctl->final_bar, 0, &g_wbwd_status);
+    }
+    __syncwarp();
   } else if (warp < 8) {
     // ---------------------------------------------------------- elementwise
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_s = t_lane + T_S + 64 * half, t_dp = t_lane + T_DP + 64 * half;
     // tiles without a visible pair first: nothing in flight depends on them
-    for (long long i = blockIdx.x; i < a.items; i += gridDim.x) {
+    for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
       const QItem it = q_item(a, i);
       if (it.steps > 0 || it.q0 + row >= a.N) continue;
       uint4* dst = reinterpret_cast<uint4*>(a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] +
@@ -888,7 +946,7 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   const long long kv_items = static_cast<long long>(a.B) * a.Hkv * (a.tiles + static_cast<long long>(a.sink_tiles) * a.chunks);
   const long long q_items = static_cast<long long>(a.B) * a.H * a.tiles;
   const long long sink_elems = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * (D / 4);
-  if (blocks > 0x7fffffffLL || kv_items > 0x7fffffffLL || sink_elems / 256 > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;
+  if (blocks > 0x7fffffffLL || kv_items > 0x7fffffffLL || q_items > 0x7fffffffLL || sink_elems / 256 > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;
   dot_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(d);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
 
@@ -900,7 +958,7 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
     kv.sh[w] = stride(a.Hkv, outs[w]->stride_h);
     kv.sn[w] = stride(a.N, outs[w]->stride_n);
   }
-  kv.items = kv_items;
+  kv.items = static_cast<unsigned>(kv_items);
   dkdv_kernel<D><<<static_cast<unsigned>(kv_items), kThreads, kv_smem, s>>>(mq, mk, mv, mo, kv);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   if (a.sink_tiles > 0) {
@@ -913,7 +971,7 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   qa.sb[0] = stride(a.B, dq->stride_b);
   qa.sh[0] = stride(a.H, dq->stride_h);
   qa.sn[0] = stride(a.N, dq->stride_n);
-  qa.items = q_items;
+  qa.items = static_cast<unsigned>(q_items);
   const long long sms = sm_count();
   dq_kernel<D><<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, q_smem, s>>>(mq, mk, mv, mo, qa);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
