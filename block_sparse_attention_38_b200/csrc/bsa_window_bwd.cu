@@ -36,8 +36,9 @@ namespace wbwd {
 
 using namespace bsa::win;
 
-constexpr int kThreads = 384;            // 8 elementwise warps, MMA, producer, 2 idle
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftWarps = 16;           // elementwise: four per TMEM lane quadrant, 32 columns each
+constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kThreads = 18 * 32;
 constexpr int kMaxChunks = 32;
 
 __device__ unsigned int g_wbwd_status;
@@ -48,6 +49,7 @@ struct Args {
   const float* Dq;           // [B, H, N]
   __nv_bfloat16* out[2];     // dV, dK, or dQ
   long long sb[2], sh[2], sn[2];
+  int wide[2];               // the outputs' rows are 32-byte aligned
   float* part;               // [B * Hkv, sink tiles, 1 + chunks, 2, 128, d]
   int B, H, N;
   unsigned Hkv, G, tiles;
@@ -85,8 +87,8 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_smem, uint32_
                         static_cast<uint32_t>(bd), static_cast<uint32_t>(bd >> 32), idesc);
 }
 
-// C (+)= A B with A in TMEM (bf16 pairs; columns 64 h .. 64 h + 31 hold entries
-// 64 h .. 64 h + 63 of the summed index) and B a tile read MN-major.  narrow: the
+// C (+)= A B with A in TMEM (bf16 pairs; columns 32 h .. 32 h + 15 hold entries
+// 32 h .. 32 h + 31 of the summed index) and B a tile read MN-major.  narrow: the
 // first 32 entries only.
 template <int D>
 __device__ __forceinline__ void mma_ts(uint32_t c_tmem, uint32_t a_tmem, uint32_t b_smem, bool narrow, bool add) {
@@ -95,39 +97,42 @@ __device__ __forceinline__ void mma_ts(uint32_t c_tmem, uint32_t a_tmem, uint32_
   const uint32_t lo = static_cast<uint32_t>(bd), hi = static_cast<uint32_t>(bd >> 32);
   umma_pv_slices2(c_tmem, a_tmem, lo, hi, kIdesc, add ? 1u : 0u);
   if (narrow) return;
-  umma_pv_slices2(c_tmem, a_tmem + 16, lo + 256, hi, kIdesc, 1u);
+  umma_pv_slices2(c_tmem, a_tmem + 32, lo + 256, hi, kIdesc, 1u);
   umma_pv_slices2(c_tmem, a_tmem + 64, lo + 512, hi, kIdesc, 1u);
-  umma_pv_slices2(c_tmem, a_tmem + 80, lo + 768, hi, kIdesc, 1u);
+  umma_pv_slices2(c_tmem, a_tmem + 96, lo + 768, hi, kIdesc, 1u);
 }
 
-// 2^x of 32 scaled scores: every fourth group of four on the FMA pipe.
-__device__ __forceinline__ void exp2_four(float& a, float& b, float& c, float& d, bool poly) {
-  if (poly) {
-    exp2_poly2(a, b);
-    exp2_poly2(c, d);
-  } else {
-    a = ex2_approx(a);
-    b = ex2_approx(b);
-    c = ex2_approx(c);
-    d = ex2_approx(d);
-  }
-}
+// The n lowest bits.
+__device__ __forceinline__ uint32_t upto(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// 32 accumulator columns of this thread's row, times mul, to 32 bf16.
-__device__ __forceinline__ void store_row32(uint32_t taddr, float mul, bool zero, uint4* dst, bool write) {
-  uint32_t w[32];
-  tmem_ld32_wait(taddr, w);
-  if (!write) return;
+// Weights of columns that the row does not see become 0.
+__device__ __forceinline__ void hide(float (&p)[32], uint32_t seen) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (!zero) {
-      r.x = pack_bf16x2(__uint_as_float(w[8 * v]) * mul, __uint_as_float(w[8 * v + 1]) * mul);
-      r.y = pack_bf16x2(__uint_as_float(w[8 * v + 2]) * mul, __uint_as_float(w[8 * v + 3]) * mul);
-      r.z = pack_bf16x2(__uint_as_float(w[8 * v + 4]) * mul, __uint_as_float(w[8 * v + 5]) * mul);
-      r.w = pack_bf16x2(__uint_as_float(w[8 * v + 6]) * mul, __uint_as_float(w[8 * v + 7]) * mul);
-    }
-    dst[v] = r;
+  for (int c = 0; c < 32; ++c)
+    if (!(seen & (1u << c))) p[c] = 0.f;
+}
+
+__device__ __forceinline__ void zero16(uint32_t taddr) {
+  uint32_t z[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) z[c] = 0u;
+  tmem_st16(taddr, z);
+}
+
+// 16 accumulator columns of this thread's row, times mul, to 16 bf16.
+__device__ __forceinline__ void store_row16(uint32_t taddr, float mul, bool zero, __nv_bfloat16* dst, bool write,
+                                            bool wide) {
+  float w[16];
+  tmem_ld16f_wait(taddr, w);
+  if (!write) return;
+  uint32_t x[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) x[c] = zero ? 0u : pack_bf16x2(w[2 * c] * mul, w[2 * c + 1] * mul);
+  if (wide) {
+    store_256(dst, x);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
 
@@ -241,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->do_empty[s], 1);
     }
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->p_ready, 8);
+    mbar_init(&ctl->p_ready, kSoftWarps);
     mbar_init(&ctl->dp_full, 1);
-    mbar_init(&ctl->ds_ready, 8);
+    mbar_init(&ctl->ds_ready, kSoftWarps);
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->fix, 1);
     ctl->abort = 0;
@@ -375,74 +380,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_drain(&ctl->acc_full, 0, &g_wbwd_status);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------- elementwise
-    const int quad = warp & 3, half = warp >> 2;
-    const int row = quad * 32 + lane, k = it.k0 + row;
+    const int wu = __shfl_sync(0xffffffffu, warp, 0);  // the same for all lanes, and known to be
+    const int quad = wu & 3, part = wu >> 2;
+    const int row = quad * 32 + lane, k = it.k0 + row, kw = it.k0 + quad * 32;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t t_s = t_lane + T_S + 64 * half, t_dp = t_lane + T_DP + 64 * half;
+    const uint32_t t_s = t_lane + T_S + 32 * part, t_dp = t_lane + T_DP + 32 * part;
     // of a far chunk only the sinks' rows are used: other warps only keep step
-    const bool idle = it.slot > 0 && it.k0 + quad * 32 >= a.sinks;
-    const bool sink = k < a.sinks;
+    const bool idle = it.slot > 0 && kw >= a.sinks;
     bool ok = true;
     for (int j = 0; j < steps && ok; ++j) {
-      const int s = j & 1, q0 = (it.first + j / G) * kTile;
-      float p[64];
+      const int s = j & 1, qw = (it.first + j / G) * kTile + 32 * part;  // this thread's first query
+      // whether no key of the warp is seen by any of the 32 queries, or every one by all
+      const bool none = idle || qw + 31 < kw || qw >= it.len || (qw - (kw + 31) >= a.window && kw >= a.sinks);
+      const bool all = qw >= kw + 31 && qw + 32 <= it.len && (qw + 31 - kw < a.window || kw + 32 <= a.sinks);
+      float p[32];
       // q_full too: it orders the producer's writes of lse2 and dq before their reads
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full, j & 1) && wait(&ctl->q_full[s], (j >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      if (!idle) {
-        const bool full = q0 >= it.k0 + kTile - 1 && q0 + kTile <= it.len &&
-                          (q0 + kTile - 1 - it.k0 < a.window || it.k0 + kTile <= a.sinks);
-        tmem_ld64_wait(t_s, p);
-        const float4* l4 = reinterpret_cast<const float4*>(ctl->lse2[s] + 64 * half);
+      if (!none) {
+        tmem_ld32f_wait(t_s, p);
+        const float4* l4 = reinterpret_cast<const float4*>(ctl->lse2[s] + 32 * part);
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < 32; c += 4) {
           const float4 l = l4[c / 4];
-          p[c] = fmaf(p[c], a.scale_log2, -l.x);
-          p[c + 1] = fmaf(p[c + 1], a.scale_log2, -l.y);
-          p[c + 2] = fmaf(p[c + 2], a.scale_log2, -l.z);
-          p[c + 3] = fmaf(p[c + 3], a.scale_log2, -l.w);
-          exp2_four(p[c], p[c + 1], p[c + 2], p[c + 3], (c / 4) % 4 == 3);
+          p[c] = ex2_approx(fmaf(p[c], a.scale_log2, -l.x));
+          p[c + 1] = ex2_approx(fmaf(p[c + 1], a.scale_log2, -l.y));
+          p[c + 2] = ex2_approx(fmaf(p[c + 2], a.scale_log2, -l.z));
+          p[c + 3] = ex2_approx(fmaf(p[c + 3], a.scale_log2, -l.w));
         }
-        if (!full) {
-          // column c is query q0 + 64 half + c; visible from lo to hi
-          const int lo = k - q0 - 64 * half;
-          const int hi = min(sink ? 64 : lo + a.window, it.len - q0 - 64 * half);
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c < lo || c >= hi) p[c] = 0.f;
+        if (!all) {  // column c is query qw + c
+          const int lo = k - qw;
+          hide(p, ~upto(lo) & upto(it.len - qw) & (k < a.sinks ? ~0u : upto(lo + a.window)));
         }
-        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-        tmem_st32_wait(t_s, pk);
+        for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st16(t_s, pk);
+      } else if (!idle) {
+        zero16(t_s);
       }
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_ready);
       ok = __all_sync(0xffffffffu, wait(&ctl->dp_full, j & 1));
       if (!ok) break;
       tc_fence_after();
-      if (!idle) {
-        float x[64];
-        tmem_ld64_wait(t_dp, x);
-        const float4* d4 = reinterpret_cast<const float4*>(ctl->dq[s] + 64 * half);
-        uint32_t pk[32];
+      if (!none) {
+        const float4* d4 = reinterpret_cast<const float4*>(ctl->dq[s] + 32 * part);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 dd = d4[c / 4];
-          // a hidden pair has p = 0, and its dP may be anything
-          const float e0 = p[c] == 0.f ? 0.f : p[c] * (x[c] - dd.x);
-          const float e1 = p[c + 1] == 0.f ? 0.f : p[c + 1] * (x[c + 1] - dd.y);
-          const float e2 = p[c + 2] == 0.f ? 0.f : p[c + 2] * (x[c + 2] - dd.z);
-          const float e3 = p[c + 3] == 0.f ? 0.f : p[c + 3] * (x[c + 3] - dd.w);
-          pk[c / 2] = pack_bf16x2(e0, e1);
-          pk[c / 2 + 1] = pack_bf16x2(e2, e3);
+        for (int h = 0; h < 2; ++h) {
+          float x[16];
+          tmem_ld16f_wait(t_dp + 16 * h, x);
+          uint32_t pk[8];
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const float4 dd = d4[4 * h + c / 4];
+            x[c] = p[16 * h + c] * (x[c] - dd.x);
+            x[c + 1] = p[16 * h + c + 1] * (x[c + 1] - dd.y);
+            x[c + 2] = p[16 * h + c + 2] * (x[c + 2] - dd.z);
+            x[c + 3] = p[16 * h + c + 3] * (x[c + 3] - dd.w);
+          }
+          if (!all) {  // a hidden pair has p = 0, and its dP may be anything
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (p[16 * h + c] == 0.f) x[c] = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+          tmem_st8(t_dp + 8 * h, pk);
         }
-        tmem_st32_wait(t_dp, pk);
+      } else if (!idle) {
+        zero16(t_dp);
       }
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->ds_ready);
@@ -451,32 +465,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       tc_fence_after();
       const bool zero = steps == 0 || k >= it.len;
+      const int c0 = part * (D / 4);
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
-        const uint32_t t_acc = t_lane + (w == 0 ? T_DV : T_DK) + half * (D / 2);
+        const uint32_t t_acc = t_lane + (w == 0 ? T_DV : T_DK) + c0;
         const float mul = w == 0 ? 1.f : a.scale;
         if (it.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out[w] + it.b * a.sb[w] + it.hk * a.sh[w] +
-                                                static_cast<long long>(k) * a.sn[w] + half * (D / 2));
+          __nv_bfloat16* dst = a.out[w] + it.b * a.sb[w] + it.hk * a.sh[w] + static_cast<long long>(k) * a.sn[w] + c0;
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) store_row32(t_acc + c, mul, zero, dst + c / 8, k < a.N);
-        } else {
+          for (int c = 0; c < D / 4; c += 16) store_row16(t_acc + c, mul, zero, dst + c, k < a.N, a.wide[w]);
+        } else if (!idle) {
           const long long tile = (static_cast<long long>(it.b) * a.Hkv + it.hk) * a.sink_tiles + it.kt;
-          float* dst = a.part + (((tile * (1 + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + half * (D / 2);
-          if (!idle) {
+          float* dst = a.part + (((tile * (1 + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + c0;
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-              uint32_t x[32];
-              tmem_ld32_wait(t_acc + c, x);
+          for (int c = 0; c < D / 4; c += 16) {
+            float x[16];
+            tmem_ld16f_wait(t_acc + c, x);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!zero)
-                  f = make_float4(__uint_as_float(x[e]) * mul, __uint_as_float(x[e + 1]) * mul,
-                                  __uint_as_float(x[e + 2]) * mul, __uint_as_float(x[e + 3]) * mul);
-                *reinterpret_cast<float4*>(dst + c + e) = f;
-              }
-            }
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(dst + c + e) =
+                  zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                       : make_float4(x[e] * mul, x[e + 1] * mul, x[e + 2] * mul, x[e + 3] * mul);
           }
         }
       }
@@ -615,14 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->v_full[s], 1);
       mbar_init(&ctl->v_empty[s], 1);
       mbar_init(&ctl->dq_full[s], 1);
-      mbar_init(&ctl->dq_free[s], 8);
+      mbar_init(&ctl->dq_free[s], kSoftWarps);
     }
     mbar_init(&ctl->do_full, 1);
     mbar_init(&ctl->do_empty, 1);
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->s_free, 8);
+    mbar_init(&ctl->s_free, kSoftWarps);
     mbar_init(&ctl->dp_full, 1);
-    mbar_init(&ctl->ds_ready, 8);
+    mbar_init(&ctl->ds_ready, kSoftWarps);
     mbar_init(&ctl->fix, 1);
     mbar_init(&ctl->final_bar, 1);
     ctl->abort = 0;
@@ -745,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!arrived(&ctl->ds_ready, t & 1)) return false;
       if (lead) {
         mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP, k + s * C::TILE, narrow, !first);
+        mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP + 16, k + s * C::TILE, narrow, true);
         umma_commit(&ctl->k_empty[s]);
         if (last) umma_commit(&ctl->dq_full[buf]);
       }
@@ -772,110 +782,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_drain(&ctl->final_bar, 0, &g_wbwd_status);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------- elementwise
-    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const int wu = __shfl_sync(0xffffffffu, warp, 0);  // the same for all lanes, and known to be
+    const int quad = wu & 3, part = wu >> 2, row = quad * 32 + lane, c0 = part * (D / 4);
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t t_s = t_lane + T_S + 64 * half, t_dp = t_lane + T_DP + 64 * half;
+    const uint32_t t_s = t_lane + T_S + 32 * part, t_dp = t_lane + T_DP + 32 * part;
+    auto place = [&](const QItem& it) {
+      return a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] + static_cast<long long>(it.q0 + row) * a.sn[0] + c0;
+    };
     // tiles without a visible pair first: nothing in flight depends on them
-    for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
-      const QItem it = q_item(a, i);
-      if (it.steps > 0 || it.q0 + row >= a.N) continue;
-      uint4* dst = reinterpret_cast<uint4*>(a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] +
-                                            static_cast<long long>(it.q0 + row) * a.sn[0] + half * (D / 2));
-      for (int c = 0; c < D / 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    auto store = [&](const QItem& it, int n) {  // dQ of the n-th item
-      const int buf = n & 1, q = it.q0 + row;
+    if (a.lens != nullptr)
+      for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
+        const QItem it = q_item(a, i);
+        if (it.steps > 0 || it.q0 + row >= a.N) continue;
+        uint4* dst = reinterpret_cast<uint4*>(place(it));
+        for (int c = 0; c < D / 32; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    // what is left to do for the item before: its dQ
+    __nv_bfloat16* dst = nullptr;
+    bool live = false, write = false;
+    auto store = [&](int n) {
+      const int buf = n & 1;
       if (!warp_wait(&ctl->dq_full[buf], (n >> 1) & 1)) return false;
       tc_fence_after();
-      uint4* dst = reinterpret_cast<uint4*>(a.out[0] + it.b * a.sb[0] + it.h * a.sh[0] +
-                                            static_cast<long long>(q) * a.sn[0] + half * (D / 2));
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32)
-        store_row32(t_lane + T_DQ + buf * D + half * (D / 2) + c, a.scale, q >= it.len, dst + c / 8, q < a.N);
+      for (int c = 0; c < D / 4; c += 16)
+        store_row16(t_lane + T_DQ + buf * D + c0 + c, a.scale, !live, dst + c, write, a.wide[0]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->dq_free[buf]);
       return true;
     };
-    QWalk w;
-    w.begin(a);
-    QItem prev = w.it;
     bool ok = true;
-    float lse2 = 0.f, dd = 0.f;
-    for (uint32_t t = 0; w.valid && ok; ++t) {
-      const QItem& it = w.it;
-      const int q = it.q0 + row, k0 = it.key0(w.j);
-      if (w.j == 0) {
-        const long long at = (static_cast<long long>(it.b) * a.H + it.h) * a.N + q;
-        lse2 = q < it.len ? a.LSE[at] * kLog2e : 0.f;
-        dd = q < it.len ? a.Dq[at] : 0.f;
-      }
-      const bool narrow = w.narrow(a);
-      const bool work = !narrow || half == 0;
-      float p[64];
-      if (!(ok = warp_wait(&ctl->s_full, t & 1))) break;
-      tc_fence_after();
-      if (work) {
-        if (narrow)
-          tmem_ld32lo_wait(t_s, p);
-        else
-          tmem_ld64_wait(t_s, p);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->s_free);
-      if (work) {
-        const bool full = k0 + kTile - 1 <= it.q0 && it.q0 + kTile <= it.len &&
-                          (k0 > it.q0 + kTile - 1 - a.window || k0 + kTile <= a.sinks);
+    int n = 0;
+    uint32_t t = 0;
+    for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+      const QItem it = q_item(a, i);
+      if (it.steps == 0) continue;
+      const int q = it.q0 + row, qw = it.q0 + 32 * quad;
+      const long long at = (static_cast<long long>(it.b) * a.H + it.h) * a.N + q;
+      const float lse2 = q < it.len ? a.LSE[at] * kLog2e : 0.f;
+      const float dd = q < it.len ? a.Dq[at] : 0.f;
+      for (int j = 0; j < it.steps && ok; ++j, ++t) {
+        const int kw = it.key0(j) + 32 * part;  // this thread's first key
+        const bool narrow = j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
+        // whether no row of the warp sees any of the 32 keys, or every row all of them
+        const bool none = (narrow && part > 0) || kw > qw + 31 || (qw - (kw + 31) >= a.window && kw >= a.sinks);
+        const bool all = kw + 31 <= qw && qw + 32 <= it.len && (qw + 31 - kw < a.window || kw + 32 <= a.sinks);
+        float p[32];
+        if (!(ok = warp_wait(&ctl->s_full, t & 1))) break;
+        tc_fence_after();
+        if (!none) tmem_ld32f_wait(t_s, p);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->s_free);
+        if (!none) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          fma2(p[c], p[c + 1], a.scale_log2, -lse2);
-          fma2(p[c + 2], p[c + 3], a.scale_log2, -lse2);
-          exp2_four(p[c], p[c + 1], p[c + 2], p[c + 3], (c / 4) % 4 == 3);
+          for (int c = 0; c < 32; c += 2) {
+            fma2(p[c], p[c + 1], a.scale_log2, -lse2);
+            p[c] = ex2_approx(p[c]);
+            p[c + 1] = ex2_approx(p[c + 1]);
+          }
+          if (!all)  // column c is key kw + c
+            hide(p, q < it.len ? upto(q - kw + 1) & (~upto(q - a.window + 1 - kw) | upto(a.sinks - kw)) : 0u);
         }
-        if (!full) {
-          // column c is key k0 + 64 half + c
-          const int hi = q < it.len ? q - k0 - 64 * half : -1;
-          const int lo = q - a.window + 1 - k0 - 64 * half, sk = a.sinks - k0 - 64 * half;
+        if (!(ok = warp_wait(&ctl->dp_full, t & 1))) break;
+        tc_fence_after();
+        if (!none) {
+          uint32_t lo0[8];
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c > hi || (c < lo && c >= sk)) p[c] = 0.f;
-        }
-      }
-      if (!(ok = warp_wait(&ctl->dp_full, t & 1))) break;
-      tc_fence_after();
-      if (work) {
-        float x[64];
-        if (narrow)
-          tmem_ld32lo_wait(t_dp, x);
-        else
-          tmem_ld64_wait(t_dp, x);
-        uint32_t pk[32];
+          for (int h = 0; h < 2; ++h) {
+            float x[16];
+            tmem_ld16f_wait(t_dp + 16 * h, x);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          // a hidden pair has p = 0, and its dP may be anything
-          const float e0 = p[c] == 0.f ? 0.f : p[c] * (x[c] - dd);
-          const float e1 = p[c + 1] == 0.f ? 0.f : p[c + 1] * (x[c + 1] - dd);
-          pk[c / 2] = pack_bf16x2(e0, e1);
+            for (int c = 0; c < 16; ++c) x[c] = p[16 * h + c] * (x[c] - dd);
+            if (!all) {  // a hidden pair has p = 0, and its dP may be anything
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (p[16 * h + c] == 0.f) x[c] = 0.f;
+            }
+            // dS = hi + lo, two bf16 terms: over the keys dS adds up to about 0, so an
+            // offset that the keys share would multiply one term's rounding
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              hi[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+              lo[c] = pack_bf16x2(x[2 * c] - __uint_as_float(hi[c] << 16),
+                                  x[2 * c + 1] - __uint_as_float(hi[c] & 0xffff0000u));
+            }
+            tmem_st8(t_dp + 8 * h, hi);
+            // the low terms' columns hold dP until both halves are read
+            if (h == 0) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) lo0[c] = lo[c];
+            } else {
+              tmem_st8(t_dp + 16, lo0);
+              tmem_st8(t_dp + 24, lo);
+            }
+          }
+        } else if (!narrow) {
+          zero16(t_dp);
+          zero16(t_dp + 16);
         }
-        tmem_st32_wait(t_dp, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->ds_ready);
+        // the last tile's dQ is stored here, beside this tile's products
+        if (j == 0 && n > 0) ok = store(n - 1);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->ds_ready);
-      // the last tile's dQ is stored here, beside this tile's products
-      if (w.j == 0 && w.n > 0 && !(ok = store(prev, w.n - 1))) break;
-      if (w.last()) {
-        prev = w.it;
-        const int n = w.n;
-        w.next(a);
-        if (!w.valid) ok = store(prev, n);
-      } else {
-        w.next(a);
-      }
+      dst = place(it);
+      live = q < it.len;
+      write = q < a.N;
+      ++n;
     }
+    if (ok && n > 0) store(n - 1);
   }
   __syncwarp();
   tc_fence_before();
@@ -958,6 +980,10 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
     kv.sh[w] = stride(a.Hkv, outs[w]->stride_h);
     kv.sn[w] = stride(a.N, outs[w]->stride_n);
   }
+  auto wide = [](const void* p, long long x, long long y, long long z) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ((x | y | z) & 15) == 0;
+  };
+  for (int w = 0; w < 2; ++w) kv.wide[w] = wide(kv.out[w], kv.sb[w], kv.sh[w], kv.sn[w]);
   kv.items = static_cast<unsigned>(kv_items);
   dkdv_kernel<D><<<static_cast<unsigned>(kv_items), kThreads, kv_smem, s>>>(mq, mk, mv, mo, kv);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
@@ -971,6 +997,7 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   qa.sb[0] = stride(a.B, dq->stride_b);
   qa.sh[0] = stride(a.H, dq->stride_h);
   qa.sn[0] = stride(a.N, dq->stride_n);
+  qa.wide[0] = wide(qa.out[0], qa.sb[0], qa.sh[0], qa.sn[0]);
   qa.items = static_cast<unsigned>(q_items);
   const long long sms = sm_count();
   dq_kernel<D><<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, q_smem, s>>>(mq, mk, mv, mo, qa);
