@@ -6,17 +6,17 @@
 //   dQ_q = scale sum_k dS k_k,  dK_k = scale sum_q dS q_q,
 // the sums for dK and dV over the G query heads that share the key/value head too.
 //
-// 10 d flops a visible pair, bound by the tensor cores.  Two tile kernels, each
+// 10 d flops a visible pair, bound by the tensor cores.  Two kinds of tiles, each
 // output row produced by one CTA (no atomics, the same bits every run), at the
-// price of computing S and dP twice (14 d flops issued):
+// price of computing S and dP twice (16 d flops issued, dS K being two products):
 //   dkdv  one CTA per 128-key tile; a step is one query tile of one head:
 //           S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
-//   dq    persistent CTAs over (head, 128-query tile); a step is one key tile:
+//   dq    a CTA per run of (head, 128-query tile); a step is one key tile:
 //           S = Q K^T, dP = dO V^T;  dQ += dS K
 // P and dS go to the second products from TMEM as bf16 (2^-8 at most, like the
 // operands they meet); scores, P before that rounding and sums are fp32.
 //
-// In both, eight warps (one thread per half row) turn S into P (phase A), then dP
+// In both, sixteen warps (four threads a row) turn S into P (phase A), then dP
 // into dS (phase B), while the tensor core works on the products of the other
 // phase: dkdv issues dP(j) | dV(j), S(j+1) | dK(j), dP(j+1) | ..., so that A(j+1)
 // runs beside dK(j) and dP(j+1), and B(j) beside dV(j) and S(j+1).  The order of
@@ -142,30 +142,42 @@ struct DotArgs {
   long long osb, osh, osn, gsb, gsh, gsn;
   float* D;
   long long rows;
-  int H, N;
+  unsigned H, N;
 };
+
+constexpr int kDotRows = 4;  // rows a lane group, whose loads are all issued before the first is used
 
 template <int D>
 __global__ void __launch_bounds__(256) dot_kernel(const DotArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, part = lane % LPR;
-  const long long r = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  float acc = 0.f;
-  if (r < a.rows) {
-    const long long bh = r / a.N;
-    const long long q = r - bh * a.N, b = bh / a.H, h = bh - b * a.H;
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + b * a.osb + h * a.osh + q * a.osn + 8 * part));
-    const uint4 y = __ldg(reinterpret_cast<const uint4*>(a.g + b * a.gsb + h * a.gsh + q * a.gsn + 8 * part));
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const long long r0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * RPW * kDotRows + lane / LPR;
+  uint4 x[kDotRows], y[kDotRows];
+#pragma unroll
+  for (int i = 0; i < kDotRows; ++i) {
+    const long long r = r0 + i * RPW;
+    x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < a.rows) {
+      const unsigned bh = static_cast<unsigned>(r / a.N);
+      const long long q = r - static_cast<long long>(bh) * a.N;
+      const unsigned b = bh / a.H, h = bh - b * a.H;
+      x[i] = __ldg(reinterpret_cast<const uint4*>(a.o + b * a.osb + h * a.osh + q * a.osn + 8 * part));
+      y[i] = __ldg(reinterpret_cast<const uint4*>(a.g + b * a.gsb + h * a.gsh + q * a.gsn + 8 * part));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDotRows; ++i) {
+    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+    float acc = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       acc = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), acc);
       acc = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), acc);
     }
-  }
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (r < a.rows && part == 0) a.D[r] = acc;
+    for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (r0 + i * RPW < a.rows && part == 0) a.D[r0 + i * RPW] = acc;
+  }
 }
 
 // ------------------------------------------------------------------- dK, dV
@@ -220,21 +232,15 @@ __device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args a) {
+__device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                          const CUtensorMap& mo, const Args& a, unsigned item, unsigned char* smem) {
   using C = Cfg<D>;
   constexpr uint32_t kIdesc = idesc_bf16_f32(128, 128, false, false);
   constexpr int T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(&g_wbwd_status, BSA_STATUS_INTERNAL);
-    return;
-  }
   unsigned char *sK = smem, *sV = smem + C::TILE, *sQ = smem + 2 * C::TILE, *sO = smem + 4 * C::TILE;
   KvCtl* ctl = reinterpret_cast<KvCtl*>(smem + 6 * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const KvItem it = kv_item(a, blockIdx.x);
+  const KvItem it = kv_item(a, item);
   const int G = static_cast<int>(a.G), steps = it.count * G;
 
   if (tid == 0) {
@@ -568,12 +574,12 @@ __device__ __forceinline__ QItem q_item(const Args& a, unsigned i) {
 
 // Steps of this CTA's items, one after another.
 struct QWalk {
-  unsigned i;
+  unsigned i, stride;
   QItem it;
   int j, n;          // step of the item, and the item's number among those with steps
   bool valid;
   __device__ __forceinline__ void seek(const Args& a) {
-    for (valid = false; i < a.items; i += gridDim.x) {
+    for (valid = false; i < a.items; i += stride) {
       it = q_item(a, i);
       if (it.steps > 0) {
         valid = true;
@@ -581,8 +587,9 @@ struct QWalk {
       }
     }
   }
-  __device__ __forceinline__ void begin(const Args& a) {
-    i = blockIdx.x;
+  __device__ __forceinline__ void begin(const Args& a, unsigned first_item, unsigned step) {
+    i = first_item;
+    stride = step;
     j = n = 0;
     seek(a);
   }
@@ -590,7 +597,7 @@ struct QWalk {
     if (++j < it.steps) return;
     j = 0;
     ++n;
-    i += gridDim.x;
+    i += stride;
     seek(a);
   }
   __device__ __forceinline__ bool last() const { return j + 1 == it.steps; }
@@ -601,16 +608,11 @@ struct QWalk {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args a) {
+__device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                         const CUtensorMap& mo, const Args& a, unsigned first_item, unsigned stride,
+                                         unsigned char* smem) {
   using C = Cfg<D>;
   constexpr int T_S = 0, T_DP = 128, T_DQ = 256;  // two dQ, D columns each
-  extern __shared__ __align__(1024) unsigned char smem[];
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(&g_wbwd_status, BSA_STATUS_INTERNAL);
-    return;
-  }
   unsigned char *sQ = smem, *sO = smem + 2 * C::TILE, *sK = smem + 3 * C::TILE, *sV = smem + 5 * C::TILE;
   QCtl* ctl = reinterpret_cast<QCtl*>(smem + 7 * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------- producer
     QWalk w;
-    w.begin(a);
+    w.begin(a, first_item, stride);
     bool ok = true;
     uint32_t t = 0, items = 0, fixes = 0;  // steps, items whose tiles were issued
     for (; w.valid && ok; w.next(a)) {
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     QWalk w;
-    w.begin(a);
+    w.begin(a, first_item, stride);
     bool ok = !w.valid || scores(0, 0, true, w.narrow(a), w.last());
     uint32_t t = 0;
     while (w.valid && ok) {
@@ -793,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // tiles without a visible pair first: nothing in flight depends on them
     if (a.lens != nullptr)
-      for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
+      for (unsigned i = first_item; i < a.items; i += stride) {
         const QItem it = q_item(a, i);
         if (it.steps > 0 || it.q0 + row >= a.N) continue;
         uint4* dst = reinterpret_cast<uint4*>(place(it));
@@ -817,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int n = 0;
     uint32_t t = 0;
-    for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+    for (unsigned i = first_item; i < a.items && ok; i += stride) {
       const QItem it = q_item(a, i);
       if (it.steps == 0) continue;
       const int q = it.q0 + row, qw = it.q0 + 32 * quad;
@@ -908,6 +910,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// One launch for both: the key tiles' blocks first (their lengths differ little, but
+// a wave of them is long), then the query tiles' in runs, which fill the SMs
+// that the last key tiles leave idle (565 us as two launches, 537 as one: 32 heads x
+// 8192 x 128, window 1024).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_backward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                           const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                           const Args kv, const Args qa) {
+  extern __shared__ __align__(1024) unsigned char smem[];  // swizzle atoms need 1024 bytes
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_wbwd_status, BSA_STATUS_INTERNAL);
+    return;
+  }
+  if (blockIdx.x < kv.items)
+    dkdv_item<D>(mq, mk, mv, mo, kv, blockIdx.x, smem);
+  else
+    dq_items<D>(mq, mk, mv, mo, qa, blockIdx.x - kv.items, gridDim.x - kv.items, smem);
+}
+
 // ------------------------------------------------------------------ host side
 // How the far queries of the sinks are cut: into chunks of about a near tile's
 // length, at most kMaxChunks.
@@ -947,11 +969,12 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
       !make_map(&mv, v, a.B, a.Hkv, a.N, D) || !make_map(&mo, g, a.B, a.H, a.N, D))
     return BSA_ERR_CUDA;
   // One CTA (and its 512 TMEM columns) per SM: more than half an SM's shared memory.
-  int kv_smem = 6 * C::TILE + static_cast<int>(sizeof(KvCtl)), q_smem = 7 * C::TILE + static_cast<int>(sizeof(QCtl));
-  kv_smem = kv_smem < 120 * 1024 ? 120 * 1024 : kv_smem;
-  q_smem = q_smem < 120 * 1024 ? 120 * 1024 : q_smem;
-  if (cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem) != cudaSuccess ||
-      cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem) != cudaSuccess)
+  static_assert(6 * C::TILE + sizeof(KvCtl) <= 232448 && 7 * C::TILE + sizeof(QCtl) <= 232448, "227 KB");
+  const int kv_smem = 6 * C::TILE + static_cast<int>(sizeof(KvCtl)), q_smem = 7 * C::TILE + static_cast<int>(sizeof(QCtl));
+  int smem = kv_smem > q_smem ? kv_smem : q_smem;
+  smem = smem < 120 * 1024 ? 120 * 1024 : smem;
+  const auto kernel = window_backward_kernel<D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return BSA_ERR_CUDA;
   auto stride = [](int n, long long x) { return n > 1 ? x : 0; };
 
@@ -964,7 +987,7 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   d.rows = static_cast<long long>(a.B) * a.H * a.N;
   d.H = a.H;
   d.N = a.N;
-  const long long per = 8 * (32 / (D / 8)), blocks = (d.rows + per - 1) / per;
+  const long long per = 8 * (32 / (D / 8)) * kDotRows, blocks = (d.rows + per - 1) / per;
   const long long kv_items = static_cast<long long>(a.B) * a.Hkv * (a.tiles + static_cast<long long>(a.sink_tiles) * a.chunks);
   const long long q_items = static_cast<long long>(a.B) * a.H * a.tiles;
   const long long sink_elems = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * (D / 4);
@@ -985,13 +1008,6 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   };
   for (int w = 0; w < 2; ++w) kv.wide[w] = wide(kv.out[w], kv.sb[w], kv.sh[w], kv.sn[w]);
   kv.items = static_cast<unsigned>(kv_items);
-  dkdv_kernel<D><<<static_cast<unsigned>(kv_items), kThreads, kv_smem, s>>>(mq, mk, mv, mo, kv);
-  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  if (a.sink_tiles > 0) {
-    sink_kernel<D><<<static_cast<unsigned>((sink_elems + 255) / 256), 256, 0, s>>>(kv);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  }
-
   Args qa = a;
   qa.out[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(dq->data));
   qa.sb[0] = stride(a.B, dq->stride_b);
@@ -999,9 +1015,18 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   qa.sn[0] = stride(a.N, dq->stride_n);
   qa.wide[0] = wide(qa.out[0], qa.sb[0], qa.sh[0], qa.sn[0]);
   qa.items = static_cast<unsigned>(q_items);
-  const long long sms = sm_count();
-  dq_kernel<D><<<static_cast<unsigned>(q_items < sms ? q_items : sms), kThreads, q_smem, s>>>(mq, mk, mv, mo, qa);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  // One run of query tiles for each SM: shorter ones balance no better (537, 543 and
+  // 544 us for one, two and three at 32 heads x 8192 x 128, window 1024) and pay for
+  // more beginnings.
+  const long long sms = sm_count(), runs = q_items < sms ? q_items : sms;
+  if (kv_items + runs > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  kernel<<<static_cast<unsigned>(kv_items + runs), kThreads, smem, s>>>(mq, mk, mv, mo, kv, qa);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  if (a.sink_tiles > 0) {
+    sink_kernel<D><<<static_cast<unsigned>((sink_elems + 255) / 256), 256, 0, s>>>(kv);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  }
+  return BSA_OK;
 }
 
 }  // namespace wbwd

@@ -487,7 +487,7 @@ int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v, 
  * hold there.  workspace: device memory of at least
  * bsa_window_backward_workspace_bytes(...) bytes, 16-byte aligned, which the call
  * overwrites; calls that may run at the same time need one each.  Enqueued on
- * `stream` (three launches, four with far queries of sinks); nothing allocated or
+ * `stream` (two launches, three with far queries of sinks); nothing allocated or
  * synchronised; no atomics, so the same bits every run.  Supported values, lens
  * and strides as for the forward; BSA_ERR_BUFFER_TOO_SMALL for a short workspace.
  */
