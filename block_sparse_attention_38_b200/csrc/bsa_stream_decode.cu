@@ -23,8 +23,9 @@
 // m_kG sum_{c in G} q_c, in fp32.  For V, P^T is multiplied by the key's scale of
 // the group before its rounding to fp16 (2^-11, against 2^-8 of the bf16
 // output), and sum_k p_k m_kG is kept in fp32.  So that small or large scales
-// lose nothing to fp16's range, the running maximum is that of
-// x_k + E - 14, with 2^E the largest scale seen (E only grows, like a maximum).
+// lose nothing to fp16's range, the running maximum is that of x_k + E - 6, with
+// 2^E the largest scale seen (E only grows, like a maximum); it is raised only by
+// more than 2^8, so P times a scale stays below 2^15.
 //
 // bf16: operands by ldmatrix; P is split into two bf16 terms (P = hi + lo), so its
 // rounding costs 2^-16; the second product is free under the cache's bytes.
@@ -32,7 +33,7 @@
 // Work split: a unit is 32 (16 for bf16) neighbouring cached rows.  Warps take
 // units in turn, each with its own ring of cp.async stages: no barrier or wait
 // between warps until the end.  A (b, cached head) is given to a cluster of up
-// to 8 CTAs when there are few of them; the CTAs' (max, sum, O) are joined over
+// to 16 CTAs when there are few of them; the CTAs' (max, sum, O) are joined over
 // distributed shared memory, so one launch does it all, with no workspace and
 // the same result in every run.
 #include <cooperative_groups.h>
@@ -40,6 +41,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -54,6 +56,7 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxM = 4096;
+constexpr float kRescale = 8.f;  // log2 units by which a maximum must grow to be raised
 
 __device__ unsigned int g_sdec_status;
 
@@ -97,16 +100,21 @@ struct Cfg {
   // the CTA's own result, read by its cluster: not overlaid
   static constexpr int OUT = HEADS * (D + 2) * 4;
   static constexpr int SMEM = (RING > PART ? RING : PART) + OUT;
+  static constexpr int PER_SM = NT == 1 && (Q4 || D == 64) ? 2 : 1;  // by registers and shared memory
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Zeros instead of the source's bytes where it is not live.
+__device__ __forceinline__ void cp16_if(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp8_if(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0)
                : "memory");
 }
@@ -122,6 +130,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -193,10 +209,11 @@ struct Warp {
   using C = Cfg<D, Q4, NT>;
   // S^T columns 2t, 2t + 1 are this lane's heads in S and O
   float o[D / 16][NT][4];
-  float top[NT][2];      // running maximum, log2 units (shifted by E - 14 for 4 bits)
+  float top[NT][2];      // running maximum, log2 units (shifted by E - 6 for 4 bits)
   float sum[NT][2];      // this lane's share of the denominator
   float pm[Q4 ? C::GR : 1][NT][2];  // sum_k p_k m_kG, this lane's keys
   int e;                 // exponent of the largest value scale seen
+  float shift;           // E - 6 (4 bits), or 0
   uint32_t qf[NT][D / 16][2];
   float qs[Q4 ? C::GR : 1][NT][2];  // sum of q over a group, heads 2t, 2t + 1
   float mul[NT][2];      // from accumulator to x in log2 units
@@ -263,30 +280,40 @@ __device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long l
 }
 
 // Issues the copies of the unit that starts at cached row `row0` of the head
-// whose rows start at `base`.  Rows past the cache's end are zero-filled.
+// whose rows start at `base`: the unit's rows lie one behind another, so lane l
+// copies bytes 16 l + 512 i.  Rows past the cache's end are zero-filled.
 template <int D, bool Q4, int NT>
 __device__ __forceinline__ void load_unit(const Args& a, long long base, int row0, uint32_t st,
                                           int lane) {
   using C = Cfg<D, Q4, NT>;
-  constexpr int PIECES = C::ROW / 16;
+  constexpr int PIECES = C::ROW / 16, RPI = 32 / PIECES;  // 16-byte pieces of a row, rows an iteration
+  const int r0 = lane / PIECES, c = lane % PIECES;
+  const unsigned char* kp = a.k + (base + row0) * C::ROW + lane * 16;
+  const unsigned char* vp = a.v + (base + row0) * C::ROW + lane * 16;
+  if (row0 + C::UK <= a.L) {
 #pragma unroll
-  for (int i = lane; i < C::UK * PIECES; i += 32) {
-    const int r = i / PIECES, c = i % PIECES;
-    const bool live = row0 + r < a.L;
-    const long long off = (base + (live ? row0 + r : 0)) * C::ROW + c * 16;
-    const int at = place<D, Q4>(r, c);
-    cp16(st + at, a.k + off, live);
-    cp16(st + C::V_OFF + at, a.v + off, live);
+    for (int i = 0; i < C::UK / RPI; ++i) {
+      const int at = place<D, Q4>(i * RPI + r0, c);
+      cp16(st + at, kp + 512 * i);
+      cp16(st + C::V_OFF + at, vp + 512 * i);
+    }
+  } else {
+    for (int i = 0; i < C::UK / RPI; ++i) {
+      const bool live = row0 + i * RPI + r0 < a.L;
+      const int at = place<D, Q4>(i * RPI + r0, c);
+      cp16_if(st + at, live ? kp + 512 * i : a.k, live);
+      cp16_if(st + C::V_OFF + at, live ? vp + 512 * i : a.v, live);
+    }
   }
   if constexpr (Q4) {
     const bool live = row0 + lane < a.L;
-    const long long off = (base + (live ? row0 + lane : 0)) * C::PROW;
+    const long long off = live ? (base + row0 + lane) * C::PROW : 0;
     if constexpr (C::PROW == 16) {
-      cp16(st + C::KP_OFF + lane * 16, a.kp + off, live);
-      cp16(st + C::VP_OFF + lane * 16, a.vp + off, live);
+      cp16_if(st + C::KP_OFF + lane * 16, a.kp + off, live);
+      cp16_if(st + C::VP_OFF + lane * 16, a.vp + off, live);
     } else {
-      cp8(st + C::KP_OFF + lane * 8, a.kp + off, live);
-      cp8(st + C::VP_OFF + lane * 8, a.vp + off, live);
+      cp8_if(st + C::KP_OFF + lane * 8, a.kp + off, live);
+      cp8_if(st + C::VP_OFF + lane * 8, a.vp + off, live);
     }
   }
 }
@@ -369,8 +396,8 @@ __device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsig
       const float2 p0 = half2_of(kp[0][G]), p1 = half2_of(kp[1][G]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+        float c[4];
+        mma_f16_zero(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
                 w.qf[nt][2 * G][0], w.qf[nt][2 * G][1]);
         mma_f16(c, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u,
                 w.qf[nt][2 * G + 1][0], w.qf[nt][2 * G + 1][1]);
@@ -480,7 +507,7 @@ __device__ __forceinline__ int channel_of(int m, int i, int g) {
 }
 
 template <int D, bool Q4, int NT>
-__global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_decode_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decode_kernel(const Args a) {
   using C = Cfg<D, Q4, NT>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t bitmap[kMaxM / 32];
@@ -571,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_deco
       for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] = 0.f;
     }
   w.e = -100;
+  w.shift = 0.f;
 #pragma unroll
   for (int m = 0; m < D / 16; ++m)
 #pragma unroll
@@ -659,48 +687,51 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_deco
           }
         }
     }
-    // exponent of the unit's largest value scale
-    float shift = 0.f;
+    // The running maximum (and E) are raised only where a lane's own scores (or
+    // scales) call for it, by more than the threshold: mostly one vote is all.
+    bool want = false;
+    uint32_t big = 0u;
     if constexpr (Q4) {
       const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + C::VP_OFF + lane * C::PROW);
-      uint32_t big = 0u;
 #pragma unroll
-      for (int G = 0; G < C::GR; ++G) big = max(big, vp[G] & 0x7fffu);
-      big = __reduce_max_sync(0xffffffffu, big);
-      w.e = max(w.e, static_cast<int>(big >> 10) - 15);
-      shift = static_cast<float>(w.e - 14);
+      for (int G = 0; G < C::GR; ++G) big = __vmaxu2(big, vp[G]);
+      big &= 0x7fffu;
+      want = static_cast<int>(big >> 10) - 15 > w.e;
     }
-    float grow[NT][2];
-    bool any = false;
+    float most[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float m = -INFINITY;
+        float m = fmaxf(x[0][nt][j], x[0][nt][2 + j]);
 #pragma unroll
-        for (int s = 0; s < C::SUB; ++s) m = fmaxf(m, fmaxf(x[s][nt][j], x[s][nt][2 + j]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m += shift;
-        const float old = w.top[nt][j];
-        // never below the old shifted maximum by more than E grew: P stays in range
-        const float now = fmaxf(old, m);
-        grow[nt][j] = now == old ? 1.f : ex2(old - now);
-        any |= now != old;
-        w.top[nt][j] = now;
+        for (int s = 1; s < C::SUB; ++s) m = fmaxf(m, fmaxf(x[s][nt][j], x[s][nt][2 + j]));
+        most[nt][j] = m;
+        want |= m + w.shift > w.top[nt][j] + kRescale;
       }
-    if (__any_sync(0xffffffffu, any)) {
+    if (__any_sync(0xffffffffu, want)) {
+      if constexpr (Q4) {
+        big = __reduce_max_sync(0xffffffffu, big);
+        w.e = max(w.e, static_cast<int>(big >> 10) - 15);
+        w.shift = static_cast<float>(w.e - 6);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          w.sum[nt][j] *= grow[nt][j];
+          float m = most[nt][j];
 #pragma unroll
-          for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] *= grow[nt][j];
+          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float old = w.top[nt][j], now = fmaxf(old, m + w.shift);
+          const float f = now == old ? 1.f : ex2(old - now);
+          w.top[nt][j] = now;
+          w.sum[nt][j] *= f;
 #pragma unroll
-          for (int m = 0; m < D / 16; ++m) {
-            w.o[m][nt][j] *= grow[nt][j];
-            w.o[m][nt][2 + j] *= grow[nt][j];
+          for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] *= f;
+#pragma unroll
+          for (int m2 = 0; m2 < D / 16; ++m2) {
+            w.o[m2][nt][j] *= f;
+            w.o[m2][nt][2 + j] *= f;
           }
         }
     }
@@ -710,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_deco
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float top = w.top[nt][i & 1];
-          const float p = ex2(x[s][nt][i] - (top == -INFINITY ? 0.f : top));
+          // the maximum is finite: every unit shows a key
+          const float p = ex2(x[s][nt][i] - w.top[nt][i & 1]);
           x[s][nt][i] = p;
           w.sum[nt][i & 1] += p;
         }
@@ -814,16 +845,53 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 && Q4) ? 2 : 1) stream_deco
   cluster.sync();  // no CTA leaves while another reads its result
 }
 
+inline int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// Whether the current device runs clusters of 16 of this kernel, asked once each.
+template <int D, bool Q4, int NT>
+bool wide_clusters(int smem) {
+  static std::atomic<signed char> known[64];  // 0: not asked, 1: yes, -1: no
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  signed char k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    const auto kernel = stream_decode_kernel<D, Q4, NT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 16;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    k = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n >= 4
+            ? 1
+            : -1;
+    cudaGetLastError();  // a refusal is an answer, not an error
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k > 0;
+}
+
 template <int D, bool Q4, int NT>
 int launch(Args a, long long groups, long long max_units, cudaStream_t s) {
   using C = Cfg<D, Q4, NT>;
   const auto kernel = stream_decode_kernel<D, Q4, NT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return BSA_ERR_CUDA;
-  // CTAs per (b, cached head): enough to cover the SMs twice, while a warp
-  // keeps two units or more.
+  // CTAs per (b, cached head): as many as run at once, while a warp keeps two units.
+  const long long slots = static_cast<long long>(C::PER_SM) * sm_count();
+  const int most = wide_clusters<D, Q4, NT>(C::SMEM) ? 16 : 8;
   int n = 1;
-  while (n < 8 && groups * n < 2 * 148 && max_units > 2LL * kWarps * n) n *= 2;
+  while (2 * n <= most && groups * 2 * n <= slots && max_units >= 2LL * kWarps * 2 * n) n *= 2;
   a.cluster = n;
   const long long blocks = groups * n;
   if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
@@ -925,7 +993,8 @@ extern "C" int bsa_q4_decode(const void* q, const void* k_new, const void* v_new
   a.bs = block_size;
   a.M = cache->L / block_size;
   if (static_cast<long long>(a.Hkv) * a.M + 1 > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
-  return dispatch<true>(a, cache->B, cache->d, cache->L / 32, static_cast<cudaStream_t>(stream));
+  // a row is taken to list an eighth of its blocks: the CSR is not read on the host
+  return dispatch<true>(a, cache->B, cache->d, cache->L / 32 / 8, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int bsa_q4_window_decode(const void* q, const void* k_new, const void* v_new,
