@@ -68,70 +68,79 @@ def q4_cache(B: int, Hkv: int, L: int, d: int, device="cuda") -> Q4Cache:
     return Q4Cache(codes(), params(), codes(), params())
 
 
-def _ints(name, t, n, device):
+# The checks below run on every call and cost as much as a small kernel, so they
+# stick to cheap attributes: `dev` is a CUDA device's index.
+
+
+def _ints(name, t, n, dev):
     import torch
 
-    if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+    if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dev, dtype):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
 def _cache_arg(cache):
-    """(ctypes struct, B, Hkv, L, d, device) of a checked Q4Cache."""
+    """(ctypes struct, B, Hkv, L, d, device index) of a checked Q4Cache."""
     import torch
 
     kc, kp, vc, vp = cache
-    if kc.dim() != 4:
+    shape = kc.shape
+    if len(shape) != 4:
         raise ValueError("k_codes must be [B, Hkv, L, d/2]")
-    B, H, L, half = kc.shape
-    device = kc.device
-    if kc.shape != vc.shape or kp.shape != (B, H, L, half // 16, 2) or vp.shape != kp.shape:
-        raise ValueError("the cache's tensors must be codes [B, Hkv, L, d/2] and parameters "
-                         "[B, Hkv, L, d/32, 2], alike for keys and values")
-    for t, dtype in ((kc, torch.uint8), (vc, torch.uint8), (kp, torch.float16), (vp, torch.float16)):
-        if not t.is_cuda or t.device != device or t.dtype is not dtype or not t.is_contiguous():
-            raise ValueError("the cache's tensors must be contiguous CUDA tensors on one device, "
-                             "codes uint8 and parameters fp16")
-    arg = _Cache(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, H, L, 2 * half)
-    return arg, B, H, L, 2 * half, device
+    B, H, L, half = shape
+    dev = kc.get_device()
+    if dev < 0:
+        raise ValueError("the cache's tensors must be CUDA tensors")
+    params = (B, H, L, half // 16, 2)
+    return (_Cache(_rows("k_codes", kc, shape, dev, torch.uint8), _rows("k_params", kp, params, dev, torch.float16),
+                   _rows("v_codes", vc, shape, dev, torch.uint8), _rows("v_params", vp, params, dev, torch.float16),
+                   B, H, L, 2 * half), B, H, L, 2 * half, dev)
 
 
-def _view(name, t, shape, device):
+def _view(name, t, shape, dev):
     """bsa_view of a bf16 tensor whose last dimension is contiguous."""
     import torch
 
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_cuda or t.device != device or t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor on {device}")
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}, got {list(t.shape)}")
     sb, sh, sn, sd = t.stride()
     # the stride of a dimension of one entry is never used
-    sb, sh, sn = (0 if shape[0] == 1 else sb, 0 if shape[1] == 1 else sh, 0 if shape[2] == 1 else sn)
-    if sd != 1 or sb % 8 or sh % 8 or sn % 8:
+    if shape[0] == 1:
+        sb = 0
+    if shape[1] == 1:
+        sh = 0
+    if shape[2] == 1:
+        sn = 0
+    if sd != 1 or (sb | sh | sn) & 7:
         raise ValueError(f"{name} must have a contiguous last dimension and other strides that are "
                          "multiples of 8")
     return _View(t.data_ptr(), sb, sh, sn)
 
 
-def _rows(name, t, shape, device, dtype):
-    if tuple(t.shape) != shape or t.device != device or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
-    return t.data_ptr()
-
-
-def _call(device, name, *args):
-    """The library function `name` with `device` current, on its current stream."""
+def _call(dev, name, *args):
+    """The library function `name` with device `dev` current, on its current stream."""
     import torch
 
-    stream = torch.cuda.current_stream(device).cuda_stream
-    fn = getattr(library(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(library(), name)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, name)
+
+
+_functions = {}
 
 
 def q4_write(cache: Q4Cache, k, v, start, lens=None) -> None:
@@ -142,13 +151,13 @@ def q4_write(cache: Q4Cache, k, v, start, lens=None) -> None:
     start, lens: CUDA int32 [B].  One token of each sequence is T = 1 with
     start its position; other cached rows stay as they were.
     """
-    arg, B, H, L, d, device = _cache_arg(cache)
+    arg, B, H, L, d, dev = _cache_arg(cache)
     if k.dim() != 4:
         raise ValueError("k, v must be [B, Hkv, T, d]")
-    shape = (B, H, int(k.shape[2]), d)
-    kv, vv = _view("k", k, shape, device), _view("v", v, shape, device)
-    _call(device, "bsa_q4_write", arg, kv, vv, _ints("start", start, B, device),
-          None if lens is None else _ints("lens", lens, B, device), shape[2])
+    shape = (B, H, k.shape[2], d)
+    kv, vv = _view("k", k, shape, dev), _view("v", v, shape, dev)
+    _call(dev, "bsa_q4_write", arg, kv, vv, _ints("start", start, B, dev),
+          None if lens is None else _ints("lens", lens, B, dev), shape[2])
 
 
 def q4_read(cache: Q4Cache, start, T: int, lens=None, out=None):
@@ -159,38 +168,37 @@ def q4_read(cache: Q4Cache, start, T: int, lens=None, out=None):
     """
     import torch
 
-    arg, B, H, L, d, device = _cache_arg(cache)
+    arg, B, H, L, d, dev = _cache_arg(cache)
     shape = (B, H, int(T), d)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=device),
-               torch.empty(shape, dtype=torch.bfloat16, device=device))
+        out = tuple(cache.k_codes.new_empty(shape, dtype=torch.bfloat16) for _ in range(2))
     k, v = out
-    _call(device, "bsa_q4_read", arg, _ints("start", start, B, device),
-          None if lens is None else _ints("lens", lens, B, device), shape[2],
-          _rows("out k", k, shape, device, torch.bfloat16), _rows("out v", v, shape, device, torch.bfloat16))
+    _call(dev, "bsa_q4_read", arg, _ints("start", start, B, dev),
+          None if lens is None else _ints("lens", lens, B, dev), shape[2],
+          _rows("out k", k, shape, dev, torch.bfloat16), _rows("out v", v, shape, dev, torch.bfloat16))
     return k, v
 
 
-def _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse):
+def _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse):
     """Checked pieces every decode step shares: (q, k_new, v_new pointers, H, scale, O, LSE)."""
     import torch
 
     bf16 = torch.bfloat16
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % Hkv:
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % max(Hkv, 1):
         raise ValueError("q must be [B, H, d] with the cache's B and d, and H a multiple of its heads")
-    H = int(q.shape[1])
+    H = q.shape[1]
     if (k_new is None) != (v_new is None):
         raise ValueError("give both k_new and v_new, or neither")
-    qp = _rows("q", q, (B, H, d), device, bf16)
+    qp = _rows("q", q, (B, H, d), dev, bf16)
     kn = vn = None
     if k_new is not None:
-        kn, vn = (_rows(n, t, (B, Hkv, d), device, bf16) for n, t in (("k_new", k_new), ("v_new", v_new)))
+        kn, vn = (_rows(n, t, (B, Hkv, d), dev, bf16) for n, t in (("k_new", k_new), ("v_new", v_new)))
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=device)
-    _rows("out", out, (B, H, d), device, bf16)
-    _rows("lse", lse, (B, H), device, torch.float32)
+        lse = q.new_empty((B, H), dtype=torch.float32)
+    _rows("out", out, (B, H, d), dev, bf16)
+    _rows("lse", lse, (B, H), dev, torch.float32)
     return qp, kn, vn, H, 1.0 / math.sqrt(d) if scale is None else float(scale), out, lse
 
 
@@ -204,11 +212,11 @@ def q4_decode(q, cache: Q4Cache, seq_len, row_ptr, col_idx, block_size: int, sca
     quantised into row seq_len[b] - 1 first.  Returns (O bf16 [B, H, d], LSE
     fp32 [B, H]).
     """
-    arg, B, Hkv, L, d, device = _cache_arg(cache)
-    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
-    rp = _ints("row_ptr", row_ptr, Hkv * (L // int(block_size)) + 1, device)
-    ci = _ints("col_idx", col_idx, col_idx.numel(), device) if col_idx.numel() else rp
-    _call(device, "bsa_q4_decode", qp, kn, vn, arg, rp, ci, _ints("seq_len", seq_len, B, device), H,
+    arg, B, Hkv, L, d, dev = _cache_arg(cache)
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse)
+    rp = _ints("row_ptr", row_ptr, Hkv * (L // int(block_size)) + 1, dev)
+    ci = _ints("col_idx", col_idx, col_idx.numel(), dev) if col_idx.numel() else rp
+    _call(dev, "bsa_q4_decode", qp, kn, vn, arg, rp, ci, _ints("seq_len", seq_len, B, dev), H,
           int(block_size), scale, out.data_ptr(), lse.data_ptr())
     return out, lse
 
@@ -218,9 +226,9 @@ def q4_window_decode(q, cache: Q4Cache, seq_len, window: int, sinks: int = 0, sc
     """One decode step over a 4-bit cache with a sliding window (bsa_q4_window_decode):
     the rows k <= t = seq_len[b] - 1 with k > t - window or k < sinks; window >= L
     sees every row.  Arguments and result as `q4_decode`."""
-    arg, B, Hkv, L, d, device = _cache_arg(cache)
-    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
-    _call(device, "bsa_q4_window_decode", qp, kn, vn, arg, _ints("seq_len", seq_len, B, device), H, int(window),
+    arg, B, Hkv, L, d, dev = _cache_arg(cache)
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse)
+    _call(dev, "bsa_q4_window_decode", qp, kn, vn, arg, _ints("seq_len", seq_len, B, dev), H, int(window),
           int(sinks), scale, out.data_ptr(), lse.data_ptr())
     return out, lse
 
@@ -233,14 +241,14 @@ def window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int = 0, sca
 
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [B, Hkv, L, d]")
-    B, Hkv, L, d = (int(x) for x in k_cache.shape)
-    device = k_cache.device
-    if not k_cache.is_cuda:
+    B, Hkv, L, d = k_cache.shape
+    dev = k_cache.get_device()
+    if dev < 0:
         raise ValueError("the caches must be CUDA tensors")
-    kc, vc = (_rows(n, t, (B, Hkv, L, d), device, torch.bfloat16)
+    kc, vc = (_rows(n, t, (B, Hkv, L, d), dev, torch.bfloat16)
               for n, t in (("k_cache", k_cache), ("v_cache", v_cache)))
-    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, device, k_new, v_new, scale, out, lse)
-    _call(device, "bsa_window_decode", qp, kn, vn, kc, vc, _ints("seq_len", seq_len, B, device), B, H, Hkv, L, d,
+    qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse)
+    _call(dev, "bsa_window_decode", qp, kn, vn, kc, vc, _ints("seq_len", seq_len, B, dev), B, H, Hkv, L, d,
           int(window), int(sinks), scale, out.data_ptr(), lse.data_ptr())
     return out, lse
 
@@ -250,7 +258,7 @@ def _heads(q, k):
     if q.dim() != 4 or k.dim() != 4 or q.shape[1] % max(int(k.shape[1]), 1):
         raise ValueError("q must be [B, H, N, d] and k, v [B, Hkv, N, d], H a multiple of Hkv")
     B, H, N, d = q.shape
-    return int(B), int(H), int(k.shape[1]), int(N), int(d)
+    return B, H, k.shape[1], N, d
 
 
 def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] = None, lens=None, out=None,
@@ -267,16 +275,18 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] 
     import torch
 
     B, H, Hkv, N, d = _heads(q, k)
-    device = q.device
-    qv = _view("q", q, (B, H, N, d), device)
-    kv, vv = _view("k", k, (B, Hkv, N, d), device), _view("v", v, (B, Hkv, N, d), device)
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    qv = _view("q", q, (B, H, N, d), dev)
+    kv, vv = _view("k", k, (B, Hkv, N, d), dev), _view("v", v, (B, Hkv, N, d), dev)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
-    _call(device, "bsa_window_forward", qv, kv, vv, None if lens is None else _ints("lens", lens, B, device), B, H,
+        lse = q.new_empty((B, H, N), dtype=torch.float32)
+    _call(dev, "bsa_window_forward", qv, kv, vv, None if lens is None else _ints("lens", lens, B, dev), B, H,
           Hkv, N, d, int(window), int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
-          _view("out", out, (B, H, N, d), device), _rows("lse", lse, (B, H, N), device, torch.float32))
+          _view("out", out, (B, H, N, d), dev), _rows("lse", lse, (B, H, N), dev, torch.float32))
     return out, lse
 
 
@@ -301,21 +311,23 @@ def window_backward(q, k, v, o, do, lse, window: int, sinks: int = 0, scale: Opt
     import torch
 
     B, H, Hkv, N, d = _heads(q, k)
-    device = q.device
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
     qs, ks = (B, H, N, d), (B, Hkv, N, d)
-    views = [_view(n, t, s, device) for n, t, s in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs),
+    views = [_view(n, t, s, dev) for n, t, s in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs),
                                                     ("do", do, qs))]
     lse = lse.contiguous()
-    lp = _rows("lse", lse, (B, H, N), device, torch.float32)
+    lp = _rows("lse", lse, (B, H, N), dev, torch.float32)
     nbytes = window_backward_workspace_bytes(B, H, Hkv, N, d, int(window), int(sinks))
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    _call(device, "bsa_window_backward", *views, lp, None if lens is None else _ints("lens", lens, B, device), B, H,
+    _call(dev, "bsa_window_backward", *views, lp, None if lens is None else _ints("lens", lens, B, dev), B, H,
           Hkv, N, d, int(window), int(sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
-          _view("dq", dq, qs, device), _view("dk", dk, ks, device), _view("dv", dv, ks, device),
+          _view("dq", dq, qs, dev), _view("dk", dk, ks, dev), _view("dv", dv, ks, dev),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
