@@ -57,6 +57,7 @@ struct Args {
   unsigned sink_tiles;       // key tiles with sinks that have far queries
   unsigned chunks;           // far chunks per sink tile, of chunk_tiles query tiles
   int chunk_tiles;
+  int alone;                 // every query sees itself only
   unsigned items;
   float scale, scale_log2;
 };
@@ -454,6 +455,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               if (p[16 * h + c] == 0.f) x[c] = 0.f;
+            if (h == 0 && qw == 0) x[0] = 0.f;  // query 0 sees one key: its P is 1 whatever the score
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
@@ -470,12 +472,13 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
     if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(&ctl->acc_full, 0));
     if (ok) {
       tc_fence_after();
-      const bool zero = steps == 0 || k >= it.len;
+      const bool none = steps == 0 || k >= it.len;
       const int c0 = part * (D / 4);
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         const uint32_t t_acc = t_lane + (w == 0 ? T_DV : T_DK) + c0;
         const float mul = w == 0 ? 1.f : a.scale;
+        const bool zero = none || (w == 1 && a.alone);
         if (it.slot < 0) {
           __nv_bfloat16* dst = a.out[w] + it.b * a.sb[w] + it.hk * a.sh[w] + static_cast<long long>(k) * a.sn[w] + c0;
 #pragma unroll 1
@@ -862,7 +865,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
             if (!all) {  // a hidden pair has p = 0, and its dP may be anything
 #pragma unroll
               for (int c = 0; c < 16; ++c)
-                if (p[16 * h + c] == 0.f) x[c] = 0.f;
+                if (p[16 * h + c] == 0.f || q == 0) x[c] = 0.f;  // query 0 sees one key: dS = 0
             }
             // dS = hi + lo, two bf16 terms: over the keys dS adds up to about 0, so an
             // offset that the keys share would multiply one term's rounding
@@ -895,7 +898,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         if (j == 0 && n > 0) ok = store(n - 1);
       }
       dst = place(it);
-      live = q < it.len;
+      live = q < it.len && !a.alone;
       write = q < a.N;
       ++n;
     }
@@ -1073,6 +1076,8 @@ extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const b
   a.tiles = p.tiles;
   a.window = window < N ? window : N;
   a.sinks = sinks < N ? sinks : N;
+  // dQ and dK are 0 where each query sees one key, not what is left of dP - D
+  a.alone = window == 1 && sinks == 0;
   a.sink_tiles = p.sink_tiles;
   a.chunks = p.chunks;
   a.chunk_tiles = p.chunk_tiles;

@@ -557,18 +557,20 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
       if (rest.pending && !finish()) return;
     }
 
-    rest.out = a.O + it.b * a.o_sb + it.h(s) * a.o_sh + static_cast<long long>(q) * a.o_sn + half * (D / 2);
-    rest.lse = a.LSE + (static_cast<long long>(it.b) * a.H + it.h(s)) * a.N + q;
-    rest.m = m;
-    rest.l = l;
-    rest.live = q < it.len;
-    rest.write = q < a.N;
-    if (it.steps > 0) {
-      rest.pending = true;
+    Rest now;
+    now.out = a.O + it.b * a.o_sb + it.h(s) * a.o_sh + static_cast<long long>(q) * a.o_sn + half * (D / 2);
+    now.lse = a.LSE + (static_cast<long long>(it.b) * a.H + it.h(s)) * a.N + q;
+    now.m = m;
+    now.l = l;
+    now.live = q < it.len;
+    now.write = q < a.N;
+    now.pending = it.steps > 0;
+    if (now.pending) {
+      rest = now;  // the one before was stored in this item's first step
       ++items;
-    } else {
-      store_half_row<D>(rest, 0.f, t_o, false, a.wide);
-      if (half == 0 && rest.write) *rest.lse = -INFINITY;
+    } else {  // no tile of it was computed: an earlier item may still be pending
+      store_half_row<D>(now, 0.f, t_o, false, a.wide);
+      if (half == 0 && now.write) *now.lse = -INFINITY;
     }
   }
   if (rest.pending) finish();

@@ -80,6 +80,24 @@ def test_backward_of_padded_sequence_major_batches(B, H, Hkv, N, window, sinks, 
     check(run(q, k, v, do, window, sinks, lens), exact(q, k, v, do, window, sinks, d ** -0.5, lens), d ** -0.5)
 
 
+def test_backward_of_many_tiles_with_empty_ones_between():
+    """More tiles than SMs, so that one block takes tiles with and without tokens in turn."""
+    B, H, Hkv, N, d, lens = 4, 16, 4, 1900, 64, [1900, 0, 700, 1300]
+    q, k, v, do = make(B, H, Hkv, N, d, 26)
+    check(run(q, k, v, do, 150, 4, lens), exact(q, k, v, do, 150, 4, d ** -0.5, lens), d ** -0.5)
+
+
+@pytest.mark.parametrize("N,window,sinks", [(1, 5, 3), (300, 1, 0), (130, 1, 1)])
+def test_queries_that_see_one_key_have_no_gradient(N, window, sinks):
+    q, k, v, do = make(2, 4, 2, N, 128, 27)
+    dq, dk, dv = run(q, k, v, do, window, sinks)
+    want = exact(q, k, v, do, window, sinks, 128 ** -0.5)
+    check((dq, dk, dv), want, 128 ** -0.5)
+    assert float(dq[:, :, 0].abs().max()) == 0
+    if N == 1 or sinks == 0:
+        assert float(dq.abs().max()) == 0 and float(dk.abs().max()) == 0
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 0.3])
 def test_backward_scales(scale):
     q, k, v, do = make(1, 2, 1, 400, 128, 23)

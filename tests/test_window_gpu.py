@@ -76,6 +76,17 @@ def test_forward_of_padded_sequence_major_batches(B, H, Hkv, N, window, sinks, l
     check_forward(got, lse, *o.window_forward(q, k, v, window, sinks, d ** -0.5, lens))
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(16, 4, 64), (9, 3, 128)])
+def test_forward_of_many_tiles_with_empty_ones_between(H, Hkv, d):
+    """More tiles than SMs, so that one block takes tiles with and without tokens in turn."""
+    B, N, lens = 4, 1900, [1900, 0, 700, 1300]
+    q, k, v, _ = make(B, H, Hkv, N, d, 8)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got, lse = bsa.window_forward(q.cuda(), k.cuda(), v.cuda(), 150, 4, lens=n)
+    assert bsa.stream_status() == 0
+    check_forward(got, lse, *o.window_forward(q, k, v, 150, 4, d ** -0.5, lens))
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-3, 1.0])
 def test_forward_scales(scale):
     q, k, v, _ = make(1, 2, 1, 400, 128, 3)
