@@ -8,13 +8,18 @@
 //
 // 10 d flops a visible pair, bound by the tensor cores.  Two kinds of tiles, each
 // output row produced by one CTA (no atomics, the same bits every run), at the
-// price of computing S and dP twice (16 d flops issued, dS K being two products):
+// price of computing S and dP twice (14 d flops issued):
 //   dkdv  one CTA per 128-key tile; a step is one query tile of one head:
 //           S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
 //   dq    a CTA per run of (head, 128-query tile); a step is one key tile:
 //           S = Q K^T, dP = dO V^T;  dQ += dS K
 // P and dS go to the second products from TMEM as bf16 (2^-8 at most, like the
-// operands they meet); scores, P before that rounding and sums are fp32.
+// operands they meet); scores, P before that rounding and sums are fp32.  Over a
+// query's keys dS adds up to about 0, so an offset that the keys share drops out of
+// dQ but not out of dS's rounding errors, which it multiplies.  So their sum is kept
+// (fp32), and one more product in each query tile takes it off again, spread evenly
+// over the keys of the diagonal tile: that is exact for the offset, and leaves of
+// each error its product with the key's distance from its neighbours' mean.
 //
 // In both, sixteen warps (four threads a row) turn S into P (phase A), then dP
 // into dS (phase B), while the tensor core works on the products of the other
@@ -743,7 +748,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       return true;
     };
     // One step, with the next one's S before its dS is waited for.
-    auto step = [&](uint32_t t, int n, bool first, bool narrow, bool last, bool more, int nn, bool nfirst,
+    auto step = [&](uint32_t t, int n, bool first, bool narrow, bool level, bool last, bool more, int nn, bool nfirst,
                     bool nnarrow, bool nlast) {
       const int s = t & 1, buf = n & 1;
       if (first && !arrived(&ctl->do_full, n & 1)) return false;
@@ -759,7 +764,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       if (!arrived(&ctl->ds_ready, t & 1)) return false;
       if (lead) {
         mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP, k + s * C::TILE, narrow, !first);
-        mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP + 16, k + s * C::TILE, narrow, true);
+        if (level) mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP + 16, k + s * C::TILE, false, true);
         umma_commit(&ctl->k_empty[s]);
         if (last) umma_commit(&ctl->dq_full[buf]);
       }
@@ -775,11 +780,11 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         const bool narrow = w.narrow(a), first = w.j == 0;
         QWalk nx = w;
         ++nx.j;
-        ok = step(t, n, first, narrow, false, true, n, false, nx.narrow(a), nx.j + 1 == steps);
+        ok = step(t, n, first, narrow, nx.j == w.it.near, false, true, n, false, nx.narrow(a), nx.j + 1 == steps);
       }
-      const bool one = steps == 1, narrow = w.narrow(a);
+      const bool one = steps == 1, narrow = w.narrow(a), level = w.j + 1 == w.it.near;
       w.next(a);
-      ok = ok && step(t, n, one, narrow, true, w.valid, n + 1, true, w.valid && w.narrow(a), w.valid && w.last());
+      ok = ok && step(t, n, one, narrow, level, true, w.valid, n + 1, true, w.valid && w.narrow(a), w.valid && w.last());
       ++t;
     }
     if (lead) {
@@ -829,6 +834,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       const long long at = (static_cast<long long>(it.b) * a.H + it.h) * a.N + q;
       const float lse2 = q < it.len ? a.LSE[at] * kLog2e : 0.f;
       const float dd = q < it.len ? a.Dq[at] : 0.f;
+      float off = 0.f;  // sum of dS's rounding errors over this thread's keys
       for (int j = 0; j < it.steps && ok; ++j, ++t) {
         const int kw = it.key0(j) + 32 * part;  // this thread's first key
         const bool narrow = j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
@@ -855,7 +861,6 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         if (!(ok = warp_wait(&ctl->dp_full, t & 1))) break;
         tc_fence_after();
         if (!none) {
-          uint32_t lo0[8];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float x[16];
@@ -867,28 +872,28 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
               for (int c = 0; c < 16; ++c)
                 if (p[16 * h + c] == 0.f || q == 0) x[c] = 0.f;  // query 0 sees one key: dS = 0
             }
-            // dS = hi + lo, two bf16 terms: over the keys dS adds up to about 0, so an
-            // offset that the keys share would multiply one term's rounding
-            uint32_t hi[8], lo[8];
+            uint32_t pk[8];
+            float ea = 0.f, eb = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              hi[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
-              lo[c] = pack_bf16x2(x[2 * c] - __uint_as_float(hi[c] << 16),
-                                  x[2 * c + 1] - __uint_as_float(hi[c] & 0xffff0000u));
+              pk[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+              float ra = __uint_as_float(pk[c] << 16), rb = __uint_as_float(pk[c] & 0xffff0000u);
+              sub2v(ra, rb, x[2 * c], x[2 * c + 1]);
+              acc2(ea, eb, ra, rb);
             }
-            tmem_st8(t_dp + 8 * h, hi);
-            // the low terms' columns hold dP until both halves are read
-            if (h == 0) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) lo0[c] = lo[c];
-            } else {
-              tmem_st8(t_dp + 16, lo0);
-              tmem_st8(t_dp + 24, lo);
-            }
+            off += ea + eb;
+            tmem_st8(t_dp + 8 * h, pk);
           }
         } else if (!narrow) {
           zero16(t_dp);
-          zero16(t_dp + 16);
+        }
+        if (j == it.near - 1) {
+          const float share = off * (-1.f / 32.f);
+          const uint32_t both = pack_bf16x2(share, share);
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = both;
+          tmem_st16(t_dp + 16, pk);
         }
         tmem_wait_st();
         tc_fence_before();

@@ -14,6 +14,16 @@ from typing import NamedTuple, Optional
 
 from . import BsaError, _check, library  # noqa: F401  (defined before this module is imported)
 
+torch = None  # imported by the first call that takes tensors: the package loads without it
+
+
+def _load():
+    global torch
+    import torch as module
+
+    torch = module
+
+
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
 
 
@@ -57,8 +67,8 @@ class Q4Cache(NamedTuple):
 
 def q4_cache(B: int, Hkv: int, L: int, d: int, device="cuda") -> Q4Cache:
     """A 4-bit cache with room for L tokens of B sequences; every row reads back as 0."""
-    import torch
-
+    if torch is None:
+        _load()
     def codes():
         return torch.zeros((B, Hkv, L, d // 2), dtype=torch.uint8, device=device)
 
@@ -73,8 +83,6 @@ def q4_cache(B: int, Hkv: int, L: int, d: int, device="cuda") -> Q4Cache:
 
 
 def _ints(name, t, n, dev):
-    import torch
-
     if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}")
     return t.data_ptr()
@@ -88,8 +96,6 @@ def _rows(name, t, shape, dev, dtype):
 
 def _cache_arg(cache):
     """(ctypes struct, B, Hkv, L, d, device index) of a checked Q4Cache."""
-    import torch
-
     kc, kp, vc, vp = cache
     shape = kc.shape
     if len(shape) != 4:
@@ -106,8 +112,6 @@ def _cache_arg(cache):
 
 def _view(name, t, shape, dev):
     """bsa_view of a bf16 tensor whose last dimension is contiguous."""
-    import torch
-
     if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev:
         raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}, got {list(t.shape)}")
     sb, sh, sn, sd = t.stride()
@@ -126,8 +130,6 @@ def _view(name, t, shape, dev):
 
 def _call(dev, name, *args):
     """The library function `name` with device `dev` current, on its current stream."""
-    import torch
-
     fn = _functions.get(name)
     if fn is None:
         fn = _functions[name] = getattr(library(), name)
@@ -151,6 +153,8 @@ def q4_write(cache: Q4Cache, k, v, start, lens=None) -> None:
     start, lens: CUDA int32 [B].  One token of each sequence is T = 1 with
     start its position; other cached rows stay as they were.
     """
+    if torch is None:
+        _load()
     arg, B, H, L, d, dev = _cache_arg(cache)
     if k.dim() != 4:
         raise ValueError("k, v must be [B, Hkv, T, d]")
@@ -166,13 +170,15 @@ def q4_read(cache: Q4Cache, start, T: int, lens=None, out=None):
 
     out: a pair of tensors to write into.
     """
-    import torch
-
+    if torch is None:
+        _load()
     arg, B, H, L, d, dev = _cache_arg(cache)
     shape = (B, H, int(T), d)
     if out is None:
-        out = tuple(cache.k_codes.new_empty(shape, dtype=torch.bfloat16) for _ in range(2))
-    k, v = out
+        k = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
     _call(dev, "bsa_q4_read", arg, _ints("start", start, B, dev),
           None if lens is None else _ints("lens", lens, B, dev), shape[2],
           _rows("out k", k, shape, dev, torch.bfloat16), _rows("out v", v, shape, dev, torch.bfloat16))
@@ -181,8 +187,6 @@ def q4_read(cache: Q4Cache, start, T: int, lens=None, out=None):
 
 def _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse):
     """Checked pieces every decode step shares: (q, k_new, v_new pointers, H, scale, O, LSE)."""
-    import torch
-
     bf16 = torch.bfloat16
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.shape[1] % max(Hkv, 1):
         raise ValueError("q must be [B, H, d] with the cache's B and d, and H a multiple of its heads")
@@ -195,10 +199,12 @@ def _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse):
         kn, vn = (_rows(n, t, (B, Hkv, d), dev, bf16) for n, t in (("k_new", k_new), ("v_new", v_new)))
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _rows("out", out, (B, H, d), dev, bf16)
     if lse is None:
         lse = q.new_empty((B, H), dtype=torch.float32)
-    _rows("out", out, (B, H, d), dev, bf16)
-    _rows("lse", lse, (B, H), dev, torch.float32)
+    else:
+        _rows("lse", lse, (B, H), dev, torch.float32)
     return qp, kn, vn, H, 1.0 / math.sqrt(d) if scale is None else float(scale), out, lse
 
 
@@ -212,6 +218,8 @@ def q4_decode(q, cache: Q4Cache, seq_len, row_ptr, col_idx, block_size: int, sca
     quantised into row seq_len[b] - 1 first.  Returns (O bf16 [B, H, d], LSE
     fp32 [B, H]).
     """
+    if torch is None:
+        _load()
     arg, B, Hkv, L, d, dev = _cache_arg(cache)
     qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse)
     rp = _ints("row_ptr", row_ptr, Hkv * (L // int(block_size)) + 1, dev)
@@ -226,6 +234,8 @@ def q4_window_decode(q, cache: Q4Cache, seq_len, window: int, sinks: int = 0, sc
     """One decode step over a 4-bit cache with a sliding window (bsa_q4_window_decode):
     the rows k <= t = seq_len[b] - 1 with k > t - window or k < sinks; window >= L
     sees every row.  Arguments and result as `q4_decode`."""
+    if torch is None:
+        _load()
     arg, B, Hkv, L, d, dev = _cache_arg(cache)
     qp, kn, vn, H, scale, out, lse = _step(q, B, Hkv, d, dev, k_new, v_new, scale, out, lse)
     _call(dev, "bsa_q4_window_decode", qp, kn, vn, arg, _ints("seq_len", seq_len, B, dev), H, int(window),
@@ -237,8 +247,8 @@ def window_decode(q, k_cache, v_cache, seq_len, window: int, sinks: int = 0, sca
                   k_new=None, v_new=None, out=None, lse=None):
     """One decode step over a bf16 cache [B, Hkv, L, d] with a sliding window
     (bsa_window_decode); arguments and result as `q4_window_decode`."""
-    import torch
-
+    if torch is None:
+        _load()
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [B, Hkv, L, d]")
     B, Hkv, L, d = k_cache.shape
@@ -272,8 +282,8 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] 
     [B], tokens of each sequence (all N where None); rows past them give O = 0
     and LSE = -inf.  Returns (O like q, LSE fp32 [B, H, N]).
     """
-    import torch
-
+    if torch is None:
+        _load()
     B, H, Hkv, N, d = _heads(q, k)
     dev = q.get_device()
     if dev < 0:
@@ -308,8 +318,8 @@ def window_backward(q, k, v, o, do, lse, window: int, sinks: int = 0, scale: Opt
     bytes (allocated on the current stream when not given); calls that may run
     at the same time need one each.
     """
-    import torch
-
+    if torch is None:
+        _load()
     B, H, Hkv, N, d = _heads(q, k)
     dev = q.get_device()
     if dev < 0:
