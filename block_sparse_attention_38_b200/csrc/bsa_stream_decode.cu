@@ -19,8 +19,9 @@
 // the bits of c are the number c 2^-24, and of c << 4 the number 16 c 2^-24, so
 // two codes in place cost one AND.  Q is scaled per head by a power of two to
 // 2^13..2^14 (exact) and by 1/16 where a code is 16-fold, so the products are
-// exact; group G's sum is multiplied by the key's scale and the minimum adds
-// m_kG sum_{c in G} q_c, in fp32.  For V, P^T is multiplied by the key's scale of
+// exact; group G's sum is multiplied by the key's scale in fp32, and the minima
+// add m_kG sum_{c in G} q_c by a product of their own, the sum in two fp16 terms
+// (2^-22).  For V, P^T is multiplied by the key's scale of
 // the group before its rounding to fp16 (2^-11, against 2^-8 of the bf16
 // output), and sum_k p_k m_kG is kept in fp32.  So that small or large scales
 // lose nothing to fp16's range, the running maximum is that of x_k + E - 6, with
@@ -53,8 +54,6 @@ namespace sdec {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxM = 4096;
 constexpr float kRescale = 8.f;  // log2 units by which a maximum must grow to be raised
 
@@ -81,8 +80,9 @@ struct Args {
   float scale_log2;
 };
 
-template <int D, bool Q4, int NT>
+template <int D, bool Q4, int NT, int NW>
 struct Cfg {
+  static constexpr int THREADS = 32 * NW;
   static constexpr int GR = D / 32;
   static constexpr int UK = Q4 ? 32 : 16;              // keys per unit
   static constexpr int SUB = UK / 16;
@@ -93,14 +93,14 @@ struct Cfg {
   static constexpr int VP_OFF = KP_OFF + UK * PROW;
   static constexpr int STAGE = 2 * UK * (ROW + PROW);  // 5 KB and 2.5 KB (4 bits), 8 and 4 KB (bf16)
   static constexpr int STAGES = Q4 ? (D == 128 ? 2 : 3) : 3;
-  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int RING = NW * STAGES * STAGE;
   static constexpr int HEADS = 8 * NT;
   // overlaid on the ring at the end: each warp's O and (max, sum)
-  static constexpr int PART = kWarps * HEADS * (D + 2) * 4;
+  static constexpr int PART = NW * HEADS * (D + 2) * 4;
   // the CTA's own result, read by its cluster: not overlaid
   static constexpr int OUT = HEADS * (D + 2) * 4;
   static constexpr int SMEM = (RING > PART ? RING : PART) + OUT;
-  static constexpr int PER_SM = NT == 1 && (Q4 || D == 64) ? 2 : 1;  // by registers and shared memory
+  static constexpr int PER_SM = NW == 8 && NT == 1 && (Q4 || D == 64) ? 2 : 1;  // by registers and shared memory
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -138,6 +138,17 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
       "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 8 summed entries instead of 16, onto zeros or onto d.
+__device__ __forceinline__ void mma_f16_k8_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -204,9 +215,9 @@ struct Span {
   int lo, sinks;         // window: first row of the window, rows always visible
 };
 
-template <int D, bool Q4, int NT>
+template <int D, bool Q4, int NT, int NW>
 struct Warp {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
   // S^T columns 2t, 2t + 1 are this lane's heads in S and O
   float o[D / 16][NT][4];
   float top[NT][2];      // running maximum, log2 units (shifted by E - 6 for 4 bits)
@@ -215,15 +226,15 @@ struct Warp {
   int e;                 // exponent of the largest value scale seen
   float shift;           // E - 6 (4 bits), or 0
   uint32_t qf[NT][D / 16][2];
-  float qs[Q4 ? C::GR : 1][NT][2];  // sum of q over a group, heads 2t, 2t + 1
+  uint32_t qs[NT][2];    // 2^-4 sum of q over group t, head g: high and low term, behind a 0
   float mul[NT][2];      // from accumulator to x in log2 units
 };
 
 // Query operands.  Lane 4 g + t holds head g's channels.
-template <int D, bool Q4, int NT>
-__device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long long head0, int heads,
+template <int D, bool Q4, int NT, int NW>
+__device__ __forceinline__ void load_q(Warp<D, Q4, NT, NW>& w, const Args& a, long long head0, int heads,
                                        int lane) {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -248,6 +259,7 @@ __device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long l
       const float mul = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 11 + ex) << 23);  // 2^(24 - 13 + ex)
       w.mul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
       w.mul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
+      float mine = 0.f;  // of group t
 #pragma unroll
       for (int G = 0; G < C::GR; ++G) {
         const float v[8] = {q4::bf16lo(raw[G].x) * up, q4::bf16hi(raw[G].x) * up,
@@ -262,10 +274,11 @@ __device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long l
         float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s *= 0x1p-24f;
-        w.qs[G][nt][0] = __shfl_sync(0xffffffffu, s, 8 * t);
-        w.qs[G][nt][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+        if (G == t) mine = 0.0625f * s;
       }
+      const float high = __half2float(__float2half_rn(mine));
+      w.qs[nt][0] = pack_h(0.f, high);
+      w.qs[nt][1] = pack_h(0.f, mine - high);
     } else {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
@@ -282,10 +295,10 @@ __device__ __forceinline__ void load_q(Warp<D, Q4, NT>& w, const Args& a, long l
 // Issues the copies of the unit that starts at cached row `row0` of the head
 // whose rows start at `base`: the unit's rows lie one behind another, so lane l
 // copies bytes 16 l + 512 i.  Rows past the cache's end are zero-filled.
-template <int D, bool Q4, int NT>
+template <int D, bool Q4, int NT, int NW>
 __device__ __forceinline__ void load_unit(const Args& a, long long base, int row0, uint32_t st,
                                           int lane) {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
   constexpr int PIECES = C::ROW / 16, RPI = 32 / PIECES;  // 16-byte pieces of a row, rows an iteration
   const int r0 = lane / PIECES, c = lane % PIECES;
   const unsigned char* kp = a.k + (base + row0) * C::ROW + lane * 16;
@@ -320,10 +333,10 @@ __device__ __forceinline__ void load_unit(const Args& a, long long base, int row
 
 // One warp: the new token's key and value as a cached row, for the cache itself
 // (row index `row`) or for row r of a stage.
-template <int D, bool Q4, int NT, bool TO_STAGE>
+template <int D, bool Q4, int NT, int NW, bool TO_STAGE>
 __device__ __forceinline__ void put_new(const Args& a, long long bh, long long row, unsigned char* st,
                                         int r, int lane) {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const __nv_bfloat16* src = (w == 0 ? a.k_new : a.v_new) + bh * D;
@@ -363,17 +376,27 @@ __device__ __forceinline__ void put_new(const Args& a, long long bh, long long r
 }
 
 // Scores of a 16-key tile, S^T[key, head] * nothing yet: accumulator units.
-template <int D, bool Q4, int NT>
-__device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsigned char* st, int sub,
+template <int D, bool Q4, int NT, int NW>
+__device__ __forceinline__ void score_tile(const Warp<D, Q4, NT, NW>& w, const unsigned char* st, int sub,
                                            int lane, float (&x)[NT][4]) {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
   if constexpr (Q4) {
     const int r0 = sub * 16 + key_of_row(g);
+    // m_kG times the sum of q over group G: a key's parameters (s_0, m_0, s_1, ...) as
+    // they lie against (0, q sum of group 0, 0, ...)
+    uint32_t m0 = 0u, m1 = 0u;
+    if (t < C::GR) {
+      m0 = *reinterpret_cast<const uint32_t*>(st + C::KP_OFF + r0 * C::PROW + 4 * t);
+      m1 = *reinterpret_cast<const uint32_t*>(st + C::KP_OFF + (r0 + 8) * C::PROW + 4 * t);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mma_f16_k8_zero(x[nt], m0, m1, w.qs[nt][0]);
+      mma_f16_k8(x[nt], m0, m1, w.qs[nt][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[nt][i] *= 0x1p-20f;
+    }
     uint32_t kw[2][C::GR], kp[2][C::GR];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -393,7 +416,7 @@ __device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsig
 #pragma unroll
     for (int G = 0; G < C::GR; ++G) {
       const uint32_t u0 = kw[0][G], u1 = kw[1][G], v0 = u0 >> 8, v1 = u1 >> 8;
-      const float2 p0 = half2_of(kp[0][G]), p1 = half2_of(kp[1][G]);
+      const float s0 = half2_of(kp[0][G]).x, s1 = half2_of(kp[1][G]).x;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float c[4];
@@ -403,12 +426,16 @@ __device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsig
                 w.qf[nt][2 * G + 1][0], w.qf[nt][2 * G + 1][1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          x[nt][j] = fmaf(p0.x, c[j], fmaf(p0.y, w.qs[G][nt][j], x[nt][j]));
-          x[nt][2 + j] = fmaf(p1.x, c[2 + j], fmaf(p1.y, w.qs[G][nt][j], x[nt][2 + j]));
+          x[nt][j] = fmaf(s0, c[j], x[nt][j]);
+          x[nt][2 + j] = fmaf(s1, c[2 + j], x[nt][2 + j]);
         }
       }
     }
   } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       // matrices: keys 0-7 / 8-15 of channels 16kk.., then of channels 16kk + 8..
@@ -422,10 +449,10 @@ __device__ __forceinline__ void score_tile(const Warp<D, Q4, NT>& w, const unsig
 }
 
 // O^T += V^T P^T for a 16-key tile; p in the layout of score_tile.
-template <int D, bool Q4, int NT>
-__device__ __forceinline__ void value_tile(Warp<D, Q4, NT>& w, const unsigned char* st, int sub, int lane,
+template <int D, bool Q4, int NT, int NW>
+__device__ __forceinline__ void value_tile(Warp<D, Q4, NT, NW>& w, const unsigned char* st, int sub, int lane,
                                            const float (&p)[NT][4]) {
-  using C = Cfg<D, Q4, NT>;
+  using C = Cfg<D, Q4, NT, NW>;
   const int g = lane >> 2, t = lane & 3;
   if constexpr (Q4) {
     const int r0 = sub * 16 + key_of_row(g);
@@ -506,9 +533,9 @@ __device__ __forceinline__ int channel_of(int m, int i, int g) {
     return 16 * m + 8 * i + g;
 }
 
-template <int D, bool Q4, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decode_kernel(const Args a) {
-  using C = Cfg<D, Q4, NT>;
+template <int D, bool Q4, int NT, int NW>
+__global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_decode_kernel(const Args a) {
+  using C = Cfg<D, Q4, NT, NW>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t bitmap[kMaxM / 32];
   __shared__ uint16_t blocks[kMaxM];
@@ -540,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
     sp.units = sp.head_units + sp.t / C::UK + 1 - sp.first_unit;
   } else if (len > 0) {
     const int i = sp.t / a.bs, W = i / 32 + 1;
-    for (int w = tid; w < W; w += kThreads) bitmap[w] = 0u;
+    for (int w = tid; w < W; w += C::THREADS) bitmap[w] = 0u;
     __syncthreads();
     int e0 = a.row_ptr[static_cast<long long>(hkv) * a.M + i];
     int e1 = a.row_ptr[static_cast<long long>(hkv) * a.M + i + 1];
@@ -548,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
       if (tid == 0) atomicOr(&g_sdec_status, BSA_STATUS_BAD_ROW_PTR);
       e0 = e1 = 0;
     }
-    for (int e = e0 + tid; e < e1; e += kThreads) {
+    for (int e = e0 + tid; e < e1; e += C::THREADS) {
       const int j = a.col_idx[e];
       if (j < 0 || j >= a.M)
         atomicOr(&g_sdec_status, BSA_STATUS_BAD_COLUMN);
@@ -579,15 +606,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
     sp.units = nb * (a.bs / C::UK);
     if (nb > 0 && blocks[nb - 1] == i) sp.units -= a.bs / C::UK - ((sp.t - i * a.bs) / C::UK + 1);
   }
+  const int per = a.row_ptr == nullptr ? 0 : 31 - __clz(a.bs / C::UK);  // log2 of a block's units
   auto row_of = [&](int u) {  // first cached row of unit u
     if (a.row_ptr == nullptr)
       return (u < sp.head_units ? u : sp.first_unit + u - sp.head_units) * C::UK;
-    const int per = a.bs / C::UK;
-    return blocks[u / per] * a.bs + (u % per) * C::UK;
+    return blocks[u >> per] * a.bs + (u & ((1 << per) - 1)) * C::UK;
   };
 
-  Warp<D, Q4, NT> w;
-  load_q<D, Q4, NT>(w, a, head0, heads, lane);
+  Warp<D, Q4, NT, NW> w;
+  load_q<D, Q4, NT, NW>(w, a, head0, heads, lane);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -608,20 +635,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
 
   // The new token's row goes into the cache once; the warp that attends to it
   // takes it from k_new / v_new again, so no order between the two is needed.
-  if (a.k_new != nullptr && len > 0 && rank == 0 && chunk == 0 && warp == kWarps - 1)
-    put_new<D, Q4, NT, false>(a, bh, base + sp.t, nullptr, 0, lane);
+  if (a.k_new != nullptr && len > 0 && rank == 0 && chunk == 0 && warp == NW - 1)
+    put_new<D, Q4, NT, NW, false>(a, bh, base + sp.t, nullptr, 0, lane);
 
   unsigned char* ring = smem + warp * C::STAGES * C::STAGE;
   const uint32_t ring_u = smem_addr(ring);
-  const int step = a.cluster * kWarps;
+  const int step = a.cluster * NW;
   const int u0 = warp * a.cluster + rank;
-  {
-    int u = u0;
+  int rows[C::STAGES];  // first rows of the units in flight
 #pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s, u += step) {
-      if (u < sp.units) load_unit<D, Q4, NT>(a, base, row_of(u), ring_u + s * C::STAGE, lane);
-      cp_commit();
-    }
+  for (int s = 0; s < C::STAGES - 1; ++s) {
+    const int u = u0 + s * step;
+    rows[s] = u < sp.units ? row_of(u) : 0;
+    if (u < sp.units) load_unit<D, Q4, NT, NW>(a, base, rows[s], ring_u + s * C::STAGE, lane);
+    cp_commit();
   }
   int slot = 0;
   for (int u = u0; u < sp.units; u += step) {
@@ -629,13 +656,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
       const int un = u + (C::STAGES - 1) * step;
       int sn = slot + C::STAGES - 1;
       if (sn >= C::STAGES) sn -= C::STAGES;
-      if (un < sp.units) load_unit<D, Q4, NT>(a, base, row_of(un), ring_u + sn * C::STAGE, lane);
+      if (un < sp.units) {
+        rows[C::STAGES - 1] = row_of(un);
+        load_unit<D, Q4, NT, NW>(a, base, rows[C::STAGES - 1], ring_u + sn * C::STAGE, lane);
+      }
       cp_commit();
     }
     cp_wait<C::STAGES - 1>();
     __syncwarp();
     unsigned char* st = ring + slot * C::STAGE;
-    const int row0 = row_of(u);
+    const int row0 = rows[0];
+#pragma unroll
+    for (int s = 0; s + 1 < C::STAGES; ++s) rows[s] = rows[s + 1];
     bool all;  // every row of the unit is visible
     if (a.row_ptr == nullptr)
       all = row0 + C::UK - 1 <= sp.t && (row0 >= sp.lo || row0 + C::UK <= sp.sinks);
@@ -647,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
     };
     if (!all || (a.k_new != nullptr && row0 + C::UK - 1 == sp.t)) {
       if (a.k_new != nullptr && row0 <= sp.t && sp.t < row0 + C::UK) {
-        put_new<D, Q4, NT, true>(a, bh, 0, st, sp.t - row0, lane);
+        put_new<D, Q4, NT, NW, true>(a, bh, 0, st, sp.t - row0, lane);
         __syncwarp();
       }
       // Hidden rows take weight 0, but 0 times what they hold (anything, NaN
@@ -668,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
 
     float x[C::SUB][NT][4];
 #pragma unroll
-    for (int s = 0; s < C::SUB; ++s) score_tile<D, Q4, NT>(w, st, s, lane, x[s]);
+    for (int s = 0; s < C::SUB; ++s) score_tile<D, Q4, NT, NW>(w, st, s, lane, x[s]);
 #pragma unroll
     for (int s = 0; s < C::SUB; ++s)
 #pragma unroll
@@ -746,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
           x[s][nt][i] = p;
           w.sum[nt][i & 1] += p;
         }
-      value_tile<D, Q4, NT>(w, st, s, lane, x[s]);
+      value_tile<D, Q4, NT, NW>(w, st, s, lane, x[s]);
     }
     __syncwarp();  // the stage is free for the next copy
     if (++slot == C::STAGES) slot = 0;
@@ -790,15 +822,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
   float* out = reinterpret_cast<float*>(smem + C::SMEM - C::OUT);
   const float* parts = reinterpret_cast<const float*>(smem);
   constexpr int PS = C::HEADS * (D + 2);
-  for (int e = tid; e < heads * D; e += kThreads) {
+  for (int e = tid; e < heads * D; e += C::THREADS) {
     const int head = e / D;
     float top = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, parts[v * PS + C::HEADS * D + head]);
+    for (int v = 0; v < NW; ++v) top = fmaxf(top, parts[v * PS + C::HEADS * D + head]);
     float o = 0.f, sum = 0.f;
     if (top != -INFINITY) {
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
+      for (int v = 0; v < NW; ++v) {
         const float m = parts[v * PS + C::HEADS * D + head];
         if (m != -INFINITY) {
           const float f = ex2(m - top);
@@ -823,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, Q4, NT>::PER_SM) stream_decod
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   const int n = a.cluster;
-  for (int e = rank * kThreads + tid; e < heads * D; e += n * kThreads) {
+  for (int e = rank * C::THREADS + tid; e < heads * D; e += n * C::THREADS) {
     const int head = e / D;
     float top = -INFINITY;
     for (int v = 0; v < n; ++v) top = fmaxf(top, cluster.map_shared_rank(out, v)[C::HEADS * D + head]);
@@ -851,61 +883,68 @@ inline int sm_count() {
   return sms;
 }
 
-// Whether the current device runs clusters of 16 of this kernel, asked once each.
-template <int D, bool Q4, int NT>
-bool wide_clusters(int smem) {
-  static std::atomic<signed char> known[64];  // 0: not asked, 1: yes, -1: no
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  signed char k = known[dev].load(std::memory_order_relaxed);
-  if (k == 0) {
-    const auto kernel = stream_decode_kernel<D, Q4, NT>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(16);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 16;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    k = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n >= 4
-            ? 1
-            : -1;
-    cudaGetLastError();  // a refusal is an answer, not an error
-    known[dev].store(k, std::memory_order_relaxed);
-  }
-  return k > 0;
-}
-
-template <int D, bool Q4, int NT>
-int launch(Args a, long long groups, long long max_units, cudaStream_t s) {
-  using C = Cfg<D, Q4, NT>;
-  const auto kernel = stream_decode_kernel<D, Q4, NT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return BSA_ERR_CUDA;
-  // CTAs per (b, cached head): as many as run at once, while a warp keeps two units.
-  const long long slots = static_cast<long long>(C::PER_SM) * sm_count();
-  const int most = wide_clusters<D, Q4, NT>(C::SMEM) ? 16 : 8;
-  int n = 1;
-  while (2 * n <= most && groups * 2 * n <= slots && max_units >= 2LL * kWarps * 2 * n) n *= 2;
-  a.cluster = n;
-  const long long blocks = groups * n;
-  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+cudaLaunchConfig_t config(long long blocks, int threads, int smem, int cluster, cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = n;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+// How many clusters of n CTAs of this kernel the current device runs at once, asked
+// once each.  A cluster sits in one GPC, so of large ones there are fewer than the
+// SMs would hold, and one too many waits for a second wave.
+constexpr int kMaxCluster = 16;
+
+template <int D, bool Q4, int NT, int NW>
+int clusters_at_once(int n) {
+  using C = Cfg<D, Q4, NT, NW>;
+  static std::atomic<int> known[64][kMaxCluster + 1];  // answer + 1; 0: not asked
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int k = known[dev][n].load(std::memory_order_relaxed);
+  if (k == 0) {
+    const auto kernel = stream_decode_kernel<D, Q4, NT, NW>;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(n, C::THREADS, C::SMEM, n, nullptr, &attr);
+    int most = 0;
+    const bool ok =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) == cudaSuccess &&
+        (n <= 8 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) &&
+        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) == cudaSuccess;
+    if (!ok) cudaGetLastError();  // a refusal is an answer, not an error
+    k = (ok ? most : 0) + 1;
+    known[dev][n].store(k, std::memory_order_relaxed);
+  }
+  return k - 1;
+}
+
+// CTAs per (b, cached head): as many as all run at once, while a warp keeps two
+// units.
+template <int D, bool Q4, int NT, int NW>
+int cluster_size(long long groups, long long max_units) {
+  int n = kMaxCluster;
+  while (n > 1 && (max_units < 2LL * NW * n || groups > clusters_at_once<D, Q4, NT, NW>(n))) --n;
+  return n;
+}
+
+template <int D, bool Q4, int NT, int NW>
+int launch(Args a, long long groups, int cluster, cudaStream_t s) {
+  using C = Cfg<D, Q4, NT, NW>;
+  const auto kernel = stream_decode_kernel<D, Q4, NT, NW>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return BSA_ERR_CUDA;
+  a.cluster = cluster;
+  const long long blocks = groups * cluster;
+  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config(blocks, C::THREADS, C::SMEM, cluster, s, &attr);
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return BSA_ERR_CUDA;
@@ -913,13 +952,27 @@ int launch(Args a, long long groups, long long max_units, cudaStream_t s) {
   return BSA_OK;
 }
 
+// A lane with one head tile of a 4-bit cache fits sixteen warps on an SM, as two CTAs
+// or as one.  Which of them puts more warps on the long axis depends on how clusters
+// of the two pack into the GPCs.
+template <int D, bool Q4, int NT>
+int launch_best(const Args& a, long long groups, long long max_units, cudaStream_t s) {
+  const int n = cluster_size<D, Q4, NT, 8>(groups, max_units);
+  if constexpr (Q4 && NT == 1) {
+    const int m = cluster_size<D, Q4, NT, 16>(groups, max_units);
+    if (groups <= sm_count() && 2 * m > n) return launch<D, Q4, NT, 16>(a, groups, m, s);
+  }
+  return launch<D, Q4, NT, 8>(a, groups, n, s);
+}
+
 template <bool Q4>
 int dispatch(Args a, int B, int d, long long max_units, cudaStream_t s) {
   const int nt = a.G > 8 ? 2 : 1;
   a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
   const long long groups = static_cast<long long>(B) * a.Hkv * a.chunks;
-  if (d == 64) return nt == 1 ? launch<64, Q4, 1>(a, groups, max_units, s) : launch<64, Q4, 2>(a, groups, max_units, s);
-  return nt == 1 ? launch<128, Q4, 1>(a, groups, max_units, s) : launch<128, Q4, 2>(a, groups, max_units, s);
+  if (d == 64)
+    return nt == 1 ? launch_best<64, Q4, 1>(a, groups, max_units, s) : launch_best<64, Q4, 2>(a, groups, max_units, s);
+  return nt == 1 ? launch_best<128, Q4, 1>(a, groups, max_units, s) : launch_best<128, Q4, 2>(a, groups, max_units, s);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
