@@ -12,7 +12,7 @@
 #include <mutex>
 
 #include "bsa.h"
-#include "sm100_ptx.cuh"
+#include "sm100_ptx_more.cuh"
 
 namespace bsa {
 namespace win {

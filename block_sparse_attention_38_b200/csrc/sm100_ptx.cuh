@@ -84,16 +84,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// 4-D tiled load global -> shared, completion counted in bytes on `bar`.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 // 3-D tiled prefetch of a box into L2 (no shared memory, no completion).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
@@ -206,26 +196,6 @@ __device__ __forceinline__ void tmem_st64_wait(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-// Loads the 128 columns at `taddr` into r as fp32 and waits for them.
-__device__ __forceinline__ void tmem_ld128_wait(uint32_t taddr, float (&r)[128]) {
-  asm volatile(
-      "{\n\ttcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128 + 64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : "=&f"(r[0]), "=&f"(r[1]), "=&f"(r[2]), "=&f"(r[3]), "=&f"(r[4]), "=&f"(r[5]), "=&f"(r[6]), "=&f"(r[7]), "=&f"(r[8]), "=&f"(r[9]), "=&f"(r[10]), "=&f"(r[11]), "=&f"(r[12]), "=&f"(r[13]), "=&f"(r[14]), "=&f"(r[15]), "=&f"(r[16]), "=&f"(r[17]), "=&f"(r[18]), "=&f"(r[19]), "=&f"(r[20]), "=&f"(r[21]), "=&f"(r[22]), "=&f"(r[23]), "=&f"(r[24]), "=&f"(r[25]), "=&f"(r[26]), "=&f"(r[27]), "=&f"(r[28]), "=&f"(r[29]), "=&f"(r[30]), "=&f"(r[31]), "=&f"(r[32]), "=&f"(r[33]), "=&f"(r[34]), "=&f"(r[35]), "=&f"(r[36]), "=&f"(r[37]), "=&f"(r[38]), "=&f"(r[39]), "=&f"(r[40]), "=&f"(r[41]), "=&f"(r[42]), "=&f"(r[43]), "=&f"(r[44]), "=&f"(r[45]), "=&f"(r[46]), "=&f"(r[47]), "=&f"(r[48]), "=&f"(r[49]), "=&f"(r[50]), "=&f"(r[51]), "=&f"(r[52]), "=&f"(r[53]), "=&f"(r[54]), "=&f"(r[55]), "=&f"(r[56]), "=&f"(r[57]), "=&f"(r[58]), "=&f"(r[59]), "=&f"(r[60]), "=&f"(r[61]), "=&f"(r[62]), "=&f"(r[63]), "=&f"(r[64]), "=&f"(r[65]), "=&f"(r[66]), "=&f"(r[67]), "=&f"(r[68]), "=&f"(r[69]), "=&f"(r[70]), "=&f"(r[71]), "=&f"(r[72]), "=&f"(r[73]), "=&f"(r[74]), "=&f"(r[75]), "=&f"(r[76]), "=&f"(r[77]), "=&f"(r[78]), "=&f"(r[79]), "=&f"(r[80]), "=&f"(r[81]), "=&f"(r[82]), "=&f"(r[83]), "=&f"(r[84]), "=&f"(r[85]), "=&f"(r[86]), "=&f"(r[87]), "=&f"(r[88]), "=&f"(r[89]), "=&f"(r[90]), "=&f"(r[91]), "=&f"(r[92]), "=&f"(r[93]), "=&f"(r[94]), "=&f"(r[95]), "=&f"(r[96]), "=&f"(r[97]), "=&f"(r[98]), "=&f"(r[99]), "=&f"(r[100]), "=&f"(r[101]), "=&f"(r[102]), "=&f"(r[103]), "=&f"(r[104]), "=&f"(r[105]), "=&f"(r[106]), "=&f"(r[107]), "=&f"(r[108]), "=&f"(r[109]), "=&f"(r[110]), "=&f"(r[111]), "=&f"(r[112]), "=&f"(r[113]), "=&f"(r[114]), "=&f"(r[115]), "=&f"(r[116]), "=&f"(r[117]), "=&f"(r[118]), "=&f"(r[119]), "=&f"(r[120]), "=&f"(r[121]), "=&f"(r[122]), "=&f"(r[123]), "=&f"(r[124]), "=&f"(r[125]), "=&f"(r[126]), "=&f"(r[127])
-      : "r"(taddr)
-      : "memory");
-}
-// Loads the 32 columns at `taddr` into r as fp32 and waits for them.
-__device__ __forceinline__ void tmem_ld32f_wait(uint32_t taddr, float (&r)[32]) {
-  asm volatile(
-      "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : "=&f"(r[0]), "=&f"(r[1]), "=&f"(r[2]), "=&f"(r[3]), "=&f"(r[4]), "=&f"(r[5]), "=&f"(r[6]), "=&f"(r[7]), "=&f"(r[8]), "=&f"(r[9]), "=&f"(r[10]), "=&f"(r[11]), "=&f"(r[12]), "=&f"(r[13]), "=&f"(r[14]), "=&f"(r[15]), "=&f"(r[16]), "=&f"(r[17]), "=&f"(r[18]), "=&f"(r[19]), "=&f"(r[20]), "=&f"(r[21]), "=&f"(r[22]), "=&f"(r[23]), "=&f"(r[24]), "=&f"(r[25]), "=&f"(r[26]), "=&f"(r[27]), "=&f"(r[28]), "=&f"(r[29]), "=&f"(r[30]), "=&f"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Loads the 32 columns at `taddr` into r and waits for them.
 __device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -242,39 +212,6 @@ __device__ __forceinline__ void tmem_st32_wait(uint32_t taddr, const uint32_t (&
       "{\n\ttcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
       "tcgen05.wait::st.sync.aligned;\n\t}"
       :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-// Loads the 16 columns at `taddr` into r as fp32 and waits for them.
-__device__ __forceinline__ void tmem_ld16f_wait(uint32_t taddr, float (&r)[16]) {
-  asm volatile(
-      "{\n\ttcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : "=&f"(r[0]), "=&f"(r[1]), "=&f"(r[2]), "=&f"(r[3]), "=&f"(r[4]), "=&f"(r[5]), "=&f"(r[6]), "=&f"(r[7]), "=&f"(r[8]), "=&f"(r[9]), "=&f"(r[10]), "=&f"(r[11]), "=&f"(r[12]), "=&f"(r[13]), "=&f"(r[14]), "=&f"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-// Stores r to the 8 columns at `taddr`; tmem_wait_st waits.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
-// Loads the 8 columns at `taddr` into r and waits for them; stores them and waits.
-__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "{\n\ttcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8_wait(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "{\n\ttcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-      "tcgen05.wait::st.sync.aligned;\n\t}"
-      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -390,32 +327,6 @@ __device__ __forceinline__ void umma_pv_chain8(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
-// Two K=16 slices of the same product.
-__device__ __forceinline__ void umma_pv_slices2(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                               uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p0, pt;\n\t.reg .b32 bl, at, one;\n\t.reg .b64 bd;\n\t"
-      "mov.b32 one, 1;\n\tsetp.eq.b32 pt, one, 1;\n\tsetp.ne.b32 p0, %5, 0;\n\t"
-      "add.s32 at, %1, 0;\n\tadd.s32 bl, %2, 0;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, p0;\n\t"
-      "add.s32 at, %1, 8;\n\tadd.s32 bl, %2, 128;\n\tmov.b64 bd, {bl, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [at], bd, %4, pt;\n\t"
-      "}"
-      :: "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(is)
-      :
-      : "memory");
-  return is != 0;
-}
-
 // Arrive once on `bar` when every tcgen05 operation issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile(
@@ -468,30 +379,6 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
 // that precedes this call.
 __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-
-// Registers per thread of a warpgroup, by all of its warps.  The shares must add
-// up to no more than the block was launched with.
-template <int N>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_less() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Orders this thread's shared-memory writes before later reads by the async
-// proxy (tcgen05.mma, TMA stores).
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// 32 bytes to a 32-byte aligned address: one full sector a lane.
-__device__ __forceinline__ void store_256(void* dst, const uint32_t (&r)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 
 // ------------------------------------------------------------------- math
