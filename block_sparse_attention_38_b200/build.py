@@ -1,4 +1,5 @@
-"""Build the C-ABI shared library libbsa.so in-tree with nvcc for sm_100a.
+"""Build the C-ABI shared library libbsa.so in-tree with nvcc for sm_100a, and the
+binding's marshalling module _bsa_torch.so with g++ against torch's headers.
 
     python -m block_sparse_attention_38_b200.build [--force] [--verbose-ptxas]
 
@@ -40,14 +41,39 @@ FLAGS = [
 ]
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+MARSHAL_SOURCE = os.path.join(CSRC, "bsa_torch.cpp")
+MARSHAL = os.path.join(HERE, "_bsa_torch.so")
+
+
+def stale(target=LIB, deps=None) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in DEPS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(p) > t for p in (DEPS if deps is None else deps))
+
+
+def build_marshal(force: bool = False) -> str:
+    """_bsa_torch.so: torch is loaded only when it has to be built."""
+    if not force and not stale(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "bsa.h")]):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    "-I" + os.path.join(ROOT, "include"), "-I" + os.path.join(at, "include"),
+                    "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), MARSHAL_SOURCE,
+                    "-o", tmp, "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                    "-lc10_cuda"], check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_marshal(force)
     if not force and not stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
