@@ -58,26 +58,32 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const CacheArgs a) {
   const long long bh = blockIdx.x / a.chunks;
   const int chunk = static_cast<int>(blockIdx.x - bh * a.chunks);
   const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<long long>(b) * a.H);
-  int first;
-  const int n = row_range(a, b, &first);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = lane % LPR;                       // channels 8x .. 8x+7
   const int G = x >> 2, z = x & 3;                // group, and this lane's place in it
   const int r0 = chunk * (kThreads / 32 * RPW * kRows) + warp * RPW + lane / LPR;
-  if (chunk * (kThreads / 32 * RPW * kRows) >= n) return;
   constexpr int kStep = kThreads / 32 * RPW;
 
   uint4 raw[kRows][2];
+  auto load = [&](int rows) {
 #pragma unroll
-  for (int p = 0; p < kRows; ++p)
+    for (int p = 0; p < kRows; ++p)
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int r = r0 + p * kStep;
-      raw[p][w] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n)
-        raw[p][w] = __ldcs(reinterpret_cast<const uint4*>(a.src[w] + b * a.sb[w] + h * a.sh[w] +
-                                                          r * a.sn[w] + 8 * x));
-    }
+      for (int w = 0; w < 2; ++w) {
+        const int r = r0 + p * kStep;
+        raw[p][w] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows)
+          raw[p][w] = __ldcs(reinterpret_cast<const uint4*>(a.src[w] + b * a.sb[w] + h * a.sh[w] +
+                                                            r * a.sn[w] + 8 * x));
+      }
+  };
+  // A few rows are loaded before their range is known, which takes a load off the
+  // latency; of many, those past a sequence's end would cost bandwidth.
+  if (a.chunks == 1) load(a.T);
+  int first;
+  const int n = row_range(a, b, &first);
+  if (chunk * (kThreads / 32 * RPW * kRows) >= n) return;
+  if (a.chunks > 1) load(n);
 #pragma unroll
   for (int p = 0; p < kRows; ++p) {
     const int r = r0 + p * kStep;

@@ -613,6 +613,19 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
     return blocks[u >> per] * a.bs + (u & ((1 << per) - 1)) * C::UK;
   };
 
+  unsigned char* ring = smem + warp * C::STAGES * C::STAGE;
+  const uint32_t ring_u = smem_addr(ring);
+  const int step = a.cluster * NW;
+  const int u0 = warp * a.cluster + rank;
+  int rows[C::STAGES];  // first rows of the units in flight
+#pragma unroll
+  for (int s = 0; s < C::STAGES - 1; ++s) {
+    const int u = u0 + s * step;
+    rows[s] = u < sp.units ? row_of(u) : 0;
+    if (u < sp.units) load_unit<D, Q4, NT, NW>(a, base, rows[s], ring_u + s * C::STAGE, lane);
+    cp_commit();
+  }
+
   Warp<D, Q4, NT, NW> w;
   load_q<D, Q4, NT, NW>(w, a, head0, heads, lane);
 #pragma unroll
@@ -638,18 +651,6 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
   if (a.k_new != nullptr && len > 0 && rank == 0 && chunk == 0 && warp == NW - 1)
     put_new<D, Q4, NT, NW, false>(a, bh, base + sp.t, nullptr, 0, lane);
 
-  unsigned char* ring = smem + warp * C::STAGES * C::STAGE;
-  const uint32_t ring_u = smem_addr(ring);
-  const int step = a.cluster * NW;
-  const int u0 = warp * a.cluster + rank;
-  int rows[C::STAGES];  // first rows of the units in flight
-#pragma unroll
-  for (int s = 0; s < C::STAGES - 1; ++s) {
-    const int u = u0 + s * step;
-    rows[s] = u < sp.units ? row_of(u) : 0;
-    if (u < sp.units) load_unit<D, Q4, NT, NW>(a, base, rows[s], ring_u + s * C::STAGE, lane);
-    cp_commit();
-  }
   int slot = 0;
   for (int u = u0; u < sp.units; u += step) {
     {
@@ -960,7 +961,7 @@ int launch_best(const Args& a, long long groups, long long max_units, cudaStream
   const int n = cluster_size<D, Q4, NT, 8>(groups, max_units);
   if constexpr (Q4 && NT == 1) {
     const int m = cluster_size<D, Q4, NT, 16>(groups, max_units);
-    if (groups <= sm_count() && 2 * m > n) return launch<D, Q4, NT, 16>(a, groups, m, s);
+    if (groups <= sm_count() && 2 * m > n && max_units >= 2LL * 16 * m) return launch<D, Q4, NT, 16>(a, groups, m, s);
   }
   return launch<D, Q4, NT, 8>(a, groups, n, s);
 }
