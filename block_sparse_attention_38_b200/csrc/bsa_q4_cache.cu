@@ -21,7 +21,8 @@ namespace bsa {
 namespace q4 {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 2;  // passes per warp
+constexpr int kRows = 2;      // passes per warp, writing
+constexpr int kReadRows = 4;  // and reading, which holds fewer registers a pass
 
 __device__ unsigned int g_q4_status;
 
@@ -130,54 +131,72 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const CacheArgs a) {
   }
 }
 
+// code * s + m of eight codes, each rounded once to bf16.  A code is taken where it
+// lies: under the exponent of 2^(23 - 4i) nibble i counts ones, so nibbles 0 to 4
+// need one logical operation each and the others one shift before it; taking the
+// power off again is exact.  (With a shift and a conversion a code the kernel was
+// bound by its instructions.)
+__device__ __forceinline__ void values8(uint32_t word, float s, float m, uint32_t (&o)[4]) {
+  const uint32_t high = word >> 12;  // nibbles 5, 6, 7 become 2, 3, 4
+  auto pair = [&](uint32_t lo, uint32_t lo_mask, uint32_t lo_power, uint32_t hi, uint32_t hi_mask, uint32_t hi_power) {
+    float x = __uint_as_float((lo & lo_mask) | lo_power), y = __uint_as_float((hi & hi_mask) | hi_power);
+    asm("{\n\t.reg .b64 v, p, t, u;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\t"
+        "sub.rn.f32x2 v, v, p;\n\tmov.b64 t, {%4, %4};\n\tmov.b64 u, {%5, %5};\n\t"
+        "fma.rn.f32x2 v, v, t, u;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(__uint_as_float(lo_power)), "f"(__uint_as_float(hi_power)), "f"(s), "f"(m));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  };
+  constexpr uint32_t k23 = 0x4b000000u, k19 = 0x49000000u, k15 = 0x47000000u, k11 = 0x45000000u, k7 = 0x43000000u;
+  o[0] = pair(word, 0xfu, k23, word, 0xf0u, k19);
+  o[1] = pair(word, 0xf00u, k15, word, 0xf000u, k11);
+  o[2] = pair(word, 0xf0000u, k7, high, 0xf00u, k15);
+  o[3] = pair(high, 0xf000u, k11, high, 0xf0000u, k7);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const CacheArgs a) {
   constexpr int LPR = D / 8;
   constexpr int RPW = 32 / LPR;
   constexpr int GR = D / kGroup;
-  const long long bh = blockIdx.x / a.chunks;
+  const unsigned bh = blockIdx.x / a.chunks;
   const int chunk = static_cast<int>(blockIdx.x - bh * a.chunks);
   const int b = static_cast<int>(bh / a.H);
   int first;
   const int n = row_range(a, b, &first);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = lane % LPR, G = x >> 2, z = x & 3;
-  const int r0 = chunk * (kThreads / 32 * RPW * kRows) + warp * RPW + lane / LPR;
+  const int r0 = chunk * (kThreads / 32 * RPW * kReadRows) + warp * RPW + lane / LPR;
   constexpr int kStep = kThreads / 32 * RPW;
+  const long long row = static_cast<long long>(bh) * a.L + first + r0;
+  const uint32_t* kc = a.codes[0] + row * (D / 8) + z * GR + G;
+  const uint16_t* vc = reinterpret_cast<const uint16_t*>(a.codes[1] + row * (D / 8)) + 2 * z * GR + G;
+  const uint32_t* kp = a.params[0] + row * GR + G;
+  const uint32_t* vp = a.params[1] + row * GR + G;
 
-  uint32_t code[kRows][2], par[kRows][2];
+  uint32_t code[kReadRows][2], par[kReadRows][2];
 #pragma unroll
-  for (int p = 0; p < kRows; ++p) {
-    const int r = r0 + p * kStep;
-    const long long row = bh * a.L + first + r;
+  for (int p = 0; p < kReadRows; ++p) {
     code[p][0] = code[p][1] = par[p][0] = par[p][1] = 0u;
-    if (r < n) {
-      code[p][0] = __ldcs(a.codes[0] + row * (D / 8) + z * GR + G);
-      const uint16_t* pc = reinterpret_cast<const uint16_t*>(a.codes[1] + row * (D / 8));
-      code[p][1] = pc[2 * z * GR + G] | static_cast<uint32_t>(pc[(2 * z + 1) * GR + G]) << 16;
-      par[p][0] = __ldcs(a.params[0] + row * GR + G);
-      par[p][1] = __ldcs(a.params[1] + row * GR + G);
+    if (r0 + p * kStep < n) {
+      code[p][0] = __ldcs(kc + p * kStep * (D / 8));
+      code[p][1] = vc[p * kStep * (D / 4)] | static_cast<uint32_t>(vc[p * kStep * (D / 4) + GR]) << 16;
+      par[p][0] = __ldcs(kp + p * kStep * GR);
+      par[p][1] = __ldcs(vp + p * kStep * GR);
     }
   }
+  const long long at = (static_cast<long long>(bh) * a.T + r0) * D + 8 * x;
+  __nv_bfloat16 *ko = a.dst[0] + at, *vo = a.dst[1] + at;
 #pragma unroll
-  for (int p = 0; p < kRows; ++p) {
-    const int r = r0 + p * kStep;
-    if (r >= a.T) continue;
+  for (int p = 0; p < kReadRows; ++p) {
+    if (r0 + p * kStep >= a.T) break;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const __half2 h = *reinterpret_cast<const __half2*>(&par[p][w]);
-      const float s = __low2float(h), m = __high2float(h);
       uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // 2^23 + code, then the code itself: no integer conversion
-        const float lo = __uint_as_float((code[p][w] >> (8 * i) & 15u) | 0x4b000000u) - 8388608.f;
-        const float hi = __uint_as_float((code[p][w] >> (8 * i + 4) & 15u) | 0x4b000000u) - 8388608.f;
-        const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(lo, s, m), fmaf(hi, s, m));
-        o[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      __stcs(reinterpret_cast<uint4*>(a.dst[w] + (bh * a.T + r) * D + 8 * x),
-             make_uint4(o[0], o[1], o[2], o[3]));
+      values8(code[p][w], __low2float(h), __high2float(h), o);
+      __stcs(reinterpret_cast<uint4*>((w == 0 ? ko : vo) + p * kStep * D), make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
 }
@@ -194,7 +213,7 @@ int check_cache(const bsa_q4_cache* c) {
   return BSA_OK;
 }
 
-void fill(CacheArgs* a, const bsa_q4_cache* c, const int32_t* start, const int32_t* lens, int T) {
+void fill(CacheArgs* a, const bsa_q4_cache* c, const int32_t* start, const int32_t* lens, int T, int passes) {
   a->codes[0] = static_cast<uint32_t*>(c->k_codes);
   a->codes[1] = static_cast<uint32_t*>(c->v_codes);
   a->params[0] = static_cast<uint32_t*>(c->k_params);
@@ -204,7 +223,7 @@ void fill(CacheArgs* a, const bsa_q4_cache* c, const int32_t* start, const int32
   a->H = c->H;
   a->L = c->L;
   a->T = T;
-  const int rows = kThreads / 32 * (c->d == 128 ? 2 : 4) * kRows;
+  const int rows = kThreads / 32 * (c->d == 128 ? 2 : 4) * passes;
   a->chunks = (T + rows - 1) / rows;
 }
 
@@ -218,7 +237,7 @@ extern "C" int bsa_q4_write(const bsa_q4_cache* cache, const bsa_view* k, const 
   if (rc != BSA_OK) return rc;
   if (!k || !v || !k->data || !v->data || !start || T < 1) return BSA_ERR_INVALID_ARG;
   CacheArgs a = {};
-  fill(&a, cache, start, lens, T);
+  fill(&a, cache, start, lens, T, kRows);
   const bsa_view* views[2] = {k, v};
   for (int w = 0; w < 2; ++w) {
     const bsa_view* x = views[w];
@@ -247,7 +266,7 @@ extern "C" int bsa_q4_read(const bsa_q4_cache* cache, const int32_t* start, cons
   if (rc != BSA_OK) return rc;
   if (!k || !v || !start || T < 1 || !aligned16(k) || !aligned16(v)) return BSA_ERR_INVALID_ARG;
   CacheArgs a = {};
-  fill(&a, cache, start, lens, T);
+  fill(&a, cache, start, lens, T, kReadRows);
   a.dst[0] = static_cast<__nv_bfloat16*>(k);
   a.dst[1] = static_cast<__nv_bfloat16*>(v);
   const long long blocks = static_cast<long long>(cache->B) * cache->H * a.chunks;
