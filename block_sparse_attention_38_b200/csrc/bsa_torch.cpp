@@ -19,6 +19,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <stdexcept>
 #include <string>
 
@@ -176,6 +177,11 @@ at::Tensor out_rows(PyObject* o, const char* name, at::IntArrayRef shape, at::Sc
 
 using Items = PyObject* const*;
 
+struct Release {
+  void operator()(PyObject* o) const { Py_DECREF(o); }
+};
+using Owned = std::unique_ptr<PyObject, Release>;
+
 PyObject* q4_write(Items a) {  // cache, k, v, start, lens
   int dev;
   const bsa_q4_cache c = cache_of(a[0], &dev);
@@ -196,18 +202,19 @@ PyObject* q4_read(Items a) {  // cache, start, T, lens, out
   const int32_t *start = ints(a[1], "start", c.B, dev), *lens = ints_or_none(a[3], "lens", c.B, dev);
   if (T < 1) refuse("T must be 1 or more");
   const int64_t shape[4] = {c.B, c.H, T, c.d};
-  PyObject *ko = Py_None, *vo = Py_None;
+  Owned ko, vo;  // a sequence may make its items anew
   if (a[4] != Py_None) {
-    if (!PySequence_Check(a[4]) || PySequence_Size(a[4]) != 2) refuse("out must be a pair of tensors");
-    ko = PySequence_GetItem(a[4], 0);
-    vo = PySequence_GetItem(a[4], 1);
-    Py_XDECREF(ko);  // the pair keeps them
-    Py_XDECREF(vo);
-    if (!ko || !vo) throw Raised();
+    const Py_ssize_t n = PySequence_Check(a[4]) ? PySequence_Size(a[4]) : 0;
+    if (n < 0) throw Raised();
+    if (n != 2) refuse("out must be a pair of tensors");
+    ko.reset(PySequence_GetItem(a[4], 0));
+    if (!ko) throw Raised();
+    vo.reset(PySequence_GetItem(a[4], 1));
+    if (!vo) throw Raised();
   }
   const at::Tensor& like = THPVariable_Unpack(PyTuple_GET_ITEM(a[0], 0));
-  at::Tensor k = out_rows(ko, "out k", shape, at::kBFloat16, like, dev);
-  at::Tensor v = out_rows(vo, "out v", shape, at::kBFloat16, like, dev);
+  at::Tensor k = out_rows(ko ? ko.get() : Py_None, "out k", shape, at::kBFloat16, like, dev);
+  at::Tensor v = out_rows(vo ? vo.get() : Py_None, "out v", shape, at::kBFloat16, like, dev);
   call(dev, "bsa_q4_read", [&](void* s) { return lib.q4_read(&c, start, lens, T, k.data_ptr(), v.data_ptr(), s); });
   return several({k, v});
 }

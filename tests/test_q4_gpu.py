@@ -135,3 +135,21 @@ def test_rows_past_two_to_the_31_bytes():
     assert bsa.stream_status() == 0
     O, _ = o.decode(q, want, want, [3], lambda b, h, t: np.arange(3), d ** -0.5)
     np.testing.assert_allclose(got.float().cpu().numpy(), O, rtol=2.0 ** -7, atol=2.0 ** -8)
+
+
+def test_out_may_be_a_sequence_that_makes_its_items():
+    """What `out` gives is held for the call, also where nothing else holds it."""
+    cache = bsa.q4_cache(1, 2, 40, 64)
+    x = torch.randn(1, 2, 40, 64, device="cuda").to(torch.bfloat16)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.q4_write(cache, x, -x, zero)
+
+    class Pair:
+        def __len__(self):
+            return 2
+
+        def __getitem__(self, i):
+            return torch.empty(1, 2, 40, 64, dtype=torch.bfloat16, device="cuda")
+
+    got, want = bsa.q4_read(cache, zero, 40, out=Pair()), bsa.q4_read(cache, zero, 40)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
