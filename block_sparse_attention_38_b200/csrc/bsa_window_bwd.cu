@@ -18,8 +18,9 @@
 // query's keys dS adds up to about 0, so an offset that the keys share drops out of
 // dQ but not out of dS's rounding errors, which it multiplies.  So their sum is kept
 // (fp32), and one more product in each query tile takes it off again, spread evenly
-// over the keys of the diagonal tile: that is exact for the offset, and leaves of
-// each error its product with the key's distance from its neighbours' mean.
+// over the keys of the diagonal tile that the query sees (the diagonal tile's own
+// errors over those of the same 32): that is exact for the offset, and leaves of each
+// error its product with the key's distance from its neighbours' mean.
 //
 // In both, sixteen warps (four threads a row) turn S into P (phase A), then dP
 // into dS (phase B), while the tensor core works on the products of the other
@@ -554,6 +555,7 @@ struct QCtl {
   uint64_t dq_full[2], dq_free[2], fix, final_bar;
   uint32_t tmem_base;
   volatile int abort;
+  float off[4][kTile];       // sums of dS's rounding errors up to the diagonal tile, of a row's four threads
 };
 
 struct QItem {
@@ -834,7 +836,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       const long long at = (static_cast<long long>(it.b) * a.H + it.h) * a.N + q;
       const float lse2 = q < it.len ? a.LSE[at] * kLog2e : 0.f;
       const float dd = q < it.len ? a.Dq[at] : 0.f;
-      float off = 0.f;  // sum of dS's rounding errors over this thread's keys
+      float off = 0.f;  // sum of dS's rounding errors over this thread's keys, before the diagonal tile and in it
       for (int j = 0; j < it.steps && ok; ++j, ++t) {
         const int kw = it.key0(j) + 32 * part;  // this thread's first key
         const bool narrow = j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
@@ -887,13 +889,30 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         } else if (!narrow) {
           zero16(t_dp);
         }
-        if (j == it.near - 1) {
-          const float share = off * (-1.f / 32.f);
-          const uint32_t both = pack_bf16x2(share, share);
-          uint32_t pk[16];
+        if (j >= it.near - 2 && j < it.near) {
+          int r = row, c0 = 32 * part;
+          asm volatile("" : "+r"(r), "+r"(c0));  // what follows is computed here, not kept from the loop's start
+          if (j == it.near - 2) {  // read at the next step, written again only after that step's ds_ready
+            ctl->off[c0 >> 5][r] = off;
+            off = 0.f;
+          } else {  // the diagonal tile: its key of column c is q - r + c
+            const int lo = max(0, r - a.window + 1), below = min(max(a.sinks - q + r, 0), lo);
+            const uint32_t seen = upto(r + 1 - c0) & (~upto(lo - c0) | upto(below - c0));
+            float share = seen ? __fdividef(-off, static_cast<float>(__popc(seen))) : 0.f;
+            if (it.near > 1) {
+              // this step's dP was issued after the last step's ds_ready of all warps: this
+              // is true at once, and orders their writes before the reads
+              mbar_try_wait(&ctl->ds_ready, (t - 1) & 1);
+              const float sum = (ctl->off[0][r] + ctl->off[1][r]) + (ctl->off[2][r] + ctl->off[3][r]);
+              share -= __fdividef(sum, static_cast<float>(r + 1 - lo + below));  // the keys that the row sees
+            }
+            const uint32_t both = pack_bf16x2(share, share);
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = both;
-          tmem_st16(t_dp + 16, pk);
+            for (int c = 0; c < 16; ++c)
+              pk[c] = both & ((seen & (1u << 2 * c) ? 0xffffu : 0u) | (seen & (2u << 2 * c) ? 0xffff0000u : 0u));
+            tmem_st16(t_dp + 16, pk);
+          }
         }
         tmem_wait_st();
         tc_fence_before();

@@ -135,3 +135,31 @@ def test_same_bits_on_two_streams_and_in_a_graph():
     torch.cuda.synchronize()
     for got in (second, third, fourth):
         assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+@pytest.mark.parametrize("H,Hkv,d,window,sinks", [(2, 1, 64, 100, 0), (2, 2, 128, 300, 0), (1, 1, 128, 40, 3)])
+def test_gradients_do_not_move_with_what_is_not_seen(H, Hkv, d, window, sinks):
+    """Large finite values in rows that a row does not meet change no bit of its
+    gradients: keys after a query or before its window, queries before a key."""
+    N, cut = 900, 333
+    q, k, v, do = (x.cuda() for x in make(1, H, Hkv, N, d, 28))
+
+    def run(q, k, v, do):
+        out, lse = bsa.window_forward(q, k, v, window, sinks)
+        return bsa.window_backward(q, k, v, out, do, lse, window, sinks)
+
+    first = run(q, k, v, do)
+    large = [x.clone() for x in (k, v)]
+    for x in large:
+        x[:, :, cut:] *= 1e6
+    assert torch.equal(run(q, *large, do)[0][:, :, :cut], first[0][:, :, :cut])
+    large = [x.clone() for x in (k, v)]
+    for x in large:
+        x[:, :, sinks:cut] *= 1e6
+    after = slice(cut + window - 1, None)
+    assert torch.equal(run(q, *large, do)[0][:, :, after], first[0][:, :, after])
+    large = [x.clone() for x in (q, do)]
+    for x in large:
+        x[:, :, :cut] *= 1e6
+    for a, b in zip(run(large[0], k, v, large[1])[1:], first[1:]):
+        assert torch.equal(a[:, :, cut:], b[:, :, cut:])
