@@ -146,3 +146,16 @@ def test_two_streams_and_a_graph_give_the_same_bits():
     torch.cuda.synchronize()
     for got in (second, third, (out, lse)):
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("Hkv,d", [(1, 64), (2, 128)])
+def test_forward_does_not_move_with_what_is_not_seen(Hkv, d):
+    """Large finite values in keys after a query, or before its window, change no bit."""
+    q, k, v, _ = (x.cuda() for x in make(1, 2, Hkv, 900, d, 9))
+    first, lse = bsa.window_forward(q, k, v, 100, 0)
+    for hidden, rows in ((slice(333, None), slice(0, 333)), (slice(0, 333), slice(333 + 99, None))):
+        far = [x.clone() for x in (k, v)]
+        for x in far:
+            x[:, :, hidden] *= 1e6
+        got, other = bsa.window_forward(q, *far, 100, 0)
+        assert torch.equal(got[:, :, rows], first[:, :, rows]) and torch.equal(other[:, :, rows], lse[:, :, rows])
