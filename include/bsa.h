@@ -463,9 +463,10 @@ int bsa_window_decode(const void* q, const void* k_new, const void* v_new, void*
  * h reads key/value head h / (H / Hkv)); LSE: device fp32 [B, H, N] contiguous.
  * lens: device int32 [B], tokens of each sequence (0..N), or NULL: N each.  Rows
  * from lens[b] on may hold anything; their O is 0 and their LSE -inf.  A bad
- * length sets BSA_STATUS_BAD_SEQ_LEN and counts as 0.  A NaN or infinity in a key
- * or value row can reach every query of the same and the next 128-query tile,
- * also those that do not see the row.
+ * length sets BSA_STATUS_BAD_SEQ_LEN and counts as 0.  A NaN or infinity in a value
+ * row inside its sequence can also reach queries that do not see the row: those
+ * up to 255 tokens before it or 384 past its window and, where its 128-row tile
+ * holds sinks, every later one (their weight for it is 0, and 0 times NaN is not).
  * Strides (of dimensions of more than one entry): positive multiples of 8, at
  * least d, below 2^39.  Any N up to 2^30, any H / Hkv; d in {64, 128}.  One
  * launch, enqueued on `stream`; nothing allocated or synchronised; the same bits
@@ -484,7 +485,9 @@ int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v, 
  * q, o, dO, dq: [B, H, N, d] views; k, v, dk, dv: [B, Hkv, N, d] views (o and LSE
  * from bsa_window_forward on the same q, k, v, lens, window, sinks and scale).
  * dq, dk, dv are written in full; rows from lens[b] on are 0, whatever the inputs
- * hold there.  workspace: device memory of at least
+ * hold there.  A NaN or infinity inside a sequence can also reach gradients of rows
+ * up to 384 tokens from those that its row meets, and of 128-row tiles with sinks.
+ * workspace: device memory of at least
  * bsa_window_backward_workspace_bytes(...) bytes, 16-byte aligned, which the call
  * overwrites; calls that may run at the same time need one each.  Enqueued on
  * `stream` (two launches, three with far queries of sinks); nothing allocated or
