@@ -27,6 +27,7 @@ namespace q4 {
 constexpr int kThreads = 256;
 constexpr int kRows = 2;      // passes per warp, writing
 constexpr int kReadRows = 4;  // and reading, which holds fewer registers a pass
+constexpr int kMaxRows = 1 << 30;  // of a cache or a call: row numbers and their ends are ints
 
 __device__ unsigned int g_q4_status;
 
@@ -213,7 +214,7 @@ int check_cache(const bsa_q4_cache* c) {
   if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) ||
       !aligned16(c->v_params))
     return BSA_ERR_INVALID_ARG;
-  if (c->d != 64 && c->d != 128) return BSA_ERR_UNSUPPORTED;
+  if ((c->d != 64 && c->d != 128) || c->L > kMaxRows) return BSA_ERR_UNSUPPORTED;
   return BSA_OK;
 }
 
@@ -240,6 +241,7 @@ extern "C" int bsa_q4_write(const bsa_q4_cache* cache, const bsa_view* k, const 
   const int rc = check_cache(cache);
   if (rc != BSA_OK) return rc;
   if (!k || !v || !k->data || !v->data || !start || T < 1) return BSA_ERR_INVALID_ARG;
+  if (T > kMaxRows) return BSA_ERR_UNSUPPORTED;
   CacheArgs a = {};
   fill(&a, cache, start, lens, T, kRows);
   const bsa_view* views[2] = {k, v};
@@ -269,6 +271,7 @@ extern "C" int bsa_q4_read(const bsa_q4_cache* cache, const int32_t* start, cons
   const int rc = check_cache(cache);
   if (rc != BSA_OK) return rc;
   if (!k || !v || !start || T < 1 || !aligned16(k) || !aligned16(v)) return BSA_ERR_INVALID_ARG;
+  if (T > kMaxRows) return BSA_ERR_UNSUPPORTED;
   CacheArgs a = {};
   fill(&a, cache, start, lens, T, kReadRows);
   a.dst[0] = static_cast<__nv_bfloat16*>(k);

@@ -992,7 +992,7 @@ int common(Args* a, const void* q, const void* k_new, const void* v_new, const i
   if (!aligned16(q) || !aligned16(O) || (k_new && (!aligned16(k_new) || !aligned16(v_new))) ||
       (reinterpret_cast<uintptr_t>(LSE) & 3u) != 0)
     return BSA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || L > (1 << 30)) return BSA_ERR_UNSUPPORTED;  // row numbers and their ends are ints
   *a = Args{};
   a->q = static_cast<const __nv_bfloat16*>(q);
   a->k_new = static_cast<const __nv_bfloat16*>(k_new);

@@ -405,8 +405,8 @@ typedef struct {
  * start = its position.  Cached rows outside those ranges are left as they were.
  * A range that is not within [0, L), or lens[b] outside [0, T], sets
  * BSA_STATUS_BAD_SEQ_LEN and writes nothing for that b.
- * Supported: d in {64, 128}.  Nothing allocated or synchronised; errors as
- * everywhere.
+ * Supported: d in {64, 128}; L and T up to 2^30.  Nothing allocated or
+ * synchronised; errors as everywhere.
  */
 int bsa_q4_write(const bsa_q4_cache* cache, const bsa_view* k, const bsa_view* v,
                  const int32_t* start, const int32_t* lens, int T, void* stream);
@@ -441,7 +441,7 @@ int bsa_q4_read(const bsa_q4_cache* cache, const int32_t* start, const int32_t* 
  * others set BSA_STATUS_BAD_SEQ_LEN and count as 0.  O: bf16 [B, H, d]; LSE:
  * fp32 [B, H].  16-byte aligned (LSE 4).  One launch, enqueued on `stream`;
  * no workspace, nothing allocated or synchronised, and the same bits every run.
- * Supported: d in {64, 128}; any H / Hkv; block_size in {32, 64, 128} with
+ * Supported: d in {64, 128}; L up to 2^30; any H / Hkv; block_size in {32, 64, 128} with
  * L % block_size == 0 and M <= 4096 (bsa_q4_decode only).
  */
 int bsa_q4_decode(const void* q, const void* k_new, const void* v_new, const bsa_q4_cache* cache,
@@ -490,7 +490,7 @@ int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bsa_view* v, 
  * workspace: device memory of at least
  * bsa_window_backward_workspace_bytes(...) bytes, 16-byte aligned, which the call
  * overwrites; calls that may run at the same time need one each.  Enqueued on
- * `stream` (two launches, three with far queries of sinks); nothing allocated or
+ * `stream` (two launches, or three where partial sums are added up); nothing allocated or
  * synchronised; no atomics, so the same bits every run.  Supported values, lens
  * and strides as for the forward; BSA_ERR_BUFFER_TOO_SMALL for a short workspace.
  */

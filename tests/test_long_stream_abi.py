@@ -215,3 +215,14 @@ def test_binding_refuses_cpu_and_broadcast_tensors():
         bsa.window_forward(torch.zeros(1, 3, 3, 64, dtype=torch.bfloat16), x, x, 2)
     with pytest.raises(ValueError):
         bsa.window_backward(x, x, x, x, x, torch.zeros(1, 2, 3), 2)
+
+
+def test_row_numbers_stay_within_an_int():
+    lib, big = bsa.library(), (1 << 30) + 1
+    c = _cache(L=big)
+    assert _write(cache=c) == bsa.ERR_UNSUPPORTED
+    assert lib.bsa_q4_read(c, P, None, 4, P, P, None) == bsa.ERR_UNSUPPORTED
+    assert lib.bsa_q4_read(_cache(), P, None, big, P, P, None) == bsa.ERR_UNSUPPORTED
+    assert _write(T=(1 << 31) - 1) == bsa.ERR_UNSUPPORTED
+    assert lib.bsa_q4_window_decode(P, None, None, c, P, 6, 8, 0, 0.1, P, P, None) == bsa.ERR_UNSUPPORTED
+    assert lib.bsa_window_decode(P, None, None, P, P, P, 2, 6, 3, big, 64, 8, 2, 0.1, P, P, None) == bsa.ERR_UNSUPPORTED
