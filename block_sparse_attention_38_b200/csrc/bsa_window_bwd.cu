@@ -9,7 +9,8 @@
 // 10 d flops a visible pair, bound by the tensor cores.  Two kinds of tiles, each
 // output row produced by one CTA (no atomics, the same bits every run), at the
 // price of computing S and dP twice (14 d flops issued):
-//   dkdv  one CTA per 128-key tile; a step is one query tile of one head:
+//   dkdv  one CTA per 128-key tile (or one each for parts of the group's heads, where
+//         key tiles are few); a step is one query tile of one head:
 //           S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
 //   dq    a CTA per run of (head, 128-query tile); a step is one key tile:
 //           S = Q K^T, dP = dO V^T;  dQ += dS K
@@ -32,7 +33,8 @@
 //
 // The keys of the sink tiles are seen by every later query.  Their far queries
 // (beyond the window) are cut into chunks that run as CTAs of their own and leave
-// fp32 partial sums in the workspace, added up in a fixed order by sink_kernel.
+// fp32 partial sums in the workspace, added up in a fixed order by sum_kernel, as are
+// those of parts of a group's heads.
 //
 // Every wait is bounded.
 #include "bsa_window.cuh"
@@ -56,12 +58,14 @@ struct Args {
   __nv_bfloat16* out[2];     // dV, dK, or dQ
   long long sb[2], sh[2], sn[2];
   int wide[2];               // the outputs' rows are 32-byte aligned
-  float* part;               // [B * Hkv, sink tiles, 1 + chunks, 2, 128, d]
+  float* part;               // [B * Hkv, part tiles, parts + chunks, 2, 128, d]
   int B, H, N;
   unsigned Hkv, G, tiles;
   int window, sinks;
   unsigned sink_tiles;       // key tiles with sinks that have far queries
   unsigned chunks;           // far chunks per sink tile, of chunk_tiles query tiles
+  unsigned parts;            // near items per key tile, of some of the group's heads each
+  unsigned part_tiles;       // key tiles whose items leave partial sums
   int chunk_tiles;
   int alone;                 // every query sees itself only
   unsigned items;
@@ -199,23 +203,32 @@ struct KvCtl {
 
 struct KvItem {
   int b, hk, kt, k0, len, slot;      // slot: the partial result's place, or -1
+  int g0, heads;                     // the group's heads that it takes
+  bool far;
   int first, count;                  // query tiles
 };
 
 __device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
   KvItem it;
-  const unsigned main_items = static_cast<unsigned>(a.B) * a.Hkv * a.tiles;
-  unsigned bh;
+  const unsigned main_items = static_cast<unsigned>(a.B) * a.Hkv * a.tiles * a.parts;
+  unsigned bh, part = 0;
   int chunk = -1;
-  if (i < main_items) {
-    bh = i / a.tiles;
-    it.kt = static_cast<int>(i - bh * a.tiles);
+  it.far = i >= main_items;
+  if (!it.far) {
+    unsigned r = i / a.parts;
+    part = i - r * a.parts;
+    bh = r / a.tiles;
+    it.kt = static_cast<int>(r - bh * a.tiles);
+    it.g0 = static_cast<int>(static_cast<unsigned long long>(part) * a.G / a.parts);
+    it.heads = static_cast<int>(static_cast<unsigned long long>(part + 1) * a.G / a.parts) - it.g0;
   } else {
     i -= main_items;
     unsigned r = i / a.chunks;
     chunk = static_cast<int>(i - r * a.chunks);
     bh = r / a.sink_tiles;
     it.kt = static_cast<int>(r - bh * a.sink_tiles);
+    it.g0 = 0;
+    it.heads = static_cast<int>(a.G);
   }
   it.b = static_cast<int>(bh / a.Hkv);
   it.hk = static_cast<int>(bh - it.b * a.Hkv);
@@ -225,14 +238,14 @@ __device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
   const int near = static_cast<int>(min(static_cast<long long>(a.tiles) - 1,
                                         (static_cast<long long>(it.k0) + kTile - 1 + a.window - 1) / kTile));
   int end;
-  if (chunk < 0) {
+  if (!it.far) {
     it.first = it.kt;
     end = min(near, last);
-    it.slot = it.kt < static_cast<int>(a.sink_tiles) ? 0 : -1;
+    it.slot = it.kt < static_cast<int>(a.part_tiles) ? static_cast<int>(part) : -1;
   } else {
     it.first = near + 1 + chunk * a.chunk_tiles;
     end = min(it.first + a.chunk_tiles - 1, last);
-    it.slot = 1 + chunk;
+    it.slot = static_cast<int>(a.parts) + chunk;
   }
   it.count = it.k0 < it.len ? max(0, end - it.first + 1) : 0;
   return it;
@@ -248,7 +261,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
   KvCtl* ctl = reinterpret_cast<KvCtl*>(smem + 6 * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvItem it = kv_item(a, item);
-  const int G = static_cast<int>(a.G), steps = it.count * G;
+  const int G = it.heads, steps = it.count * G, head0 = it.hk * static_cast<int>(a.G) + it.g0;
 
   if (tid == 0) {
     mbar_init(&ctl->kv_full, 1);
@@ -294,7 +307,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
     float lse[4], dd[4];
     auto fetch = [&](int j) {
       const int qt = j / G;
-      const long long row = (static_cast<long long>(it.b) * a.H + it.hk * G + j - qt * G) * a.N;
+      const long long row = (static_cast<long long>(it.b) * a.H + head0 + j - qt * G) * a.N;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int q = (it.first + qt) * kTile + r * 32 + lane;
@@ -305,7 +318,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
     fetch(0);
     int issued = 0;
     for (int j = 0; j < steps && ok; ++j) {
-      const int s = j & 1, qt = j / G, q0 = (it.first + qt) * kTile, h = it.hk * G + j - qt * G;
+      const int s = j & 1, qt = j / G, q0 = (it.first + qt) * kTile, h = head0 + j - qt * G;
       const bool fix = q0 + kTile > it.len && it.len < a.N;
       for (int w = 0; w < 2 && ok; ++w) {
         unsigned char* dst = (w == 0 ? sQ : sO) + s * C::TILE;
@@ -401,7 +414,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_s = t_lane + T_S + 32 * part, t_dp = t_lane + T_DP + 32 * part;
     // of a far chunk only the sinks' rows are used: other warps only keep step
-    const bool idle = it.slot > 0 && kw >= a.sinks;
+    const bool idle = it.far && kw >= a.sinks;
     bool ok = true;
     for (int j = 0; j < steps && ok; ++j) {
       const int s = j & 1, qw = (it.first + j / G) * kTile + 32 * part;  // this thread's first query
@@ -490,8 +503,8 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
 #pragma unroll 1
           for (int c = 0; c < D / 4; c += 16) store_row16(t_acc + c, mul, zero, dst + c, k < a.N, a.wide[w]);
         } else if (!idle) {
-          const long long tile = (static_cast<long long>(it.b) * a.Hkv + it.hk) * a.sink_tiles + it.kt;
-          float* dst = a.part + (((tile * (1 + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + c0;
+          const long long tile = (static_cast<long long>(it.b) * a.Hkv + it.hk) * a.part_tiles + it.kt;
+          float* dst = a.part + (((tile * (a.parts + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + c0;
 #pragma unroll 1
           for (int c = 0; c < D / 4; c += 16) {
             float x[16];
@@ -515,13 +528,13 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
   }
 }
 
-// Adds a sink tile's partial sums in a fixed order: the near queries', then each
-// far chunk's (which hold the sinks' rows only).
+// Adds a key tile's partial sums in a fixed order: the near queries' of each part of
+// the group's heads, then each far chunk's (which hold the sinks' rows only).
 template <int D>
-__global__ void __launch_bounds__(256) sink_kernel(const Args a) {
+__global__ void __launch_bounds__(256) sum_kernel(const Args a) {
   const long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;  // (tile, w, row, 4 channels)
   constexpr int Q = D / 4;
-  const long long total = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * Q;
+  const long long total = static_cast<long long>(a.B) * a.Hkv * a.part_tiles * 2 * kTile * Q;
   if (e >= total) return;
   const int c = static_cast<int>(e % Q);
   long long r = e / Q;
@@ -529,14 +542,14 @@ __global__ void __launch_bounds__(256) sink_kernel(const Args a) {
   r /= kTile;
   const int w = static_cast<int>(r % 2);
   const long long tile = r / 2;
-  const int kt = static_cast<int>(tile % a.sink_tiles), k = kt * kTile + row;
+  const int kt = static_cast<int>(tile % a.part_tiles), k = kt * kTile + row;
   if (k >= a.N) return;
-  const long long bh = tile / a.sink_tiles;
-  const int n = k < a.sinks ? 1 + static_cast<int>(a.chunks) : 1;
+  const long long bh = tile / a.part_tiles;
+  const int n = static_cast<int>(a.parts + (kt < static_cast<int>(a.sink_tiles) && k < a.sinks ? a.chunks : 0u));
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < n; ++i) {
     const float4 x = *reinterpret_cast<const float4*>(
-        a.part + (((tile * (1 + a.chunks) + i) * 2 + w) * kTile + row) * D + 4 * c);
+        a.part + (((tile * (a.parts + a.chunks) + i) * 2 + w) * kTile + row) * D + 4 * c);
     s.x += x.x;
     s.y += x.y;
     s.z += x.z;
@@ -958,10 +971,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// How the far queries of the sinks are cut: into chunks of about a near tile's
-// length, at most kMaxChunks.
+// How the far queries of the sinks are cut: into chunks of about a near item's
+// length, at most kMaxChunks.  And where key tiles are few, how the heads of a group
+// are, so that no long item is what all wait for: into parts until there are 60 items,
+// which leaves the rest of the 148 SMs to the query tiles (8 heads over 1, 4096 x 128,
+// window 1024, 4 sinks: 139 us whole; 82, 89 and 93 for 60, 85 and 148 items).  Items of
+// few steps stay whole, as a part costs a beginning and a pass over fp32 sums.
+constexpr int kItemsWanted = 60, kStepsWorthParts = 8;
+
 struct Plan {
-  int tiles, sink_tiles, chunks, chunk_tiles;
+  int tiles, sink_tiles, chunks, chunk_tiles, parts, part_tiles;
   size_t d_bytes, part_bytes;
 };
 
@@ -972,18 +991,26 @@ Plan make_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   // near query tiles of key tile t end at t + (kTile - 1 + w - 1) / kTile
   const long long near = (kTile + w - 2) / kTile;
   const long long far = p.tiles - 1 - near;  // far query tiles of key tile 0
+  const long long G = H / Hkv, items = static_cast<long long>(B) * Hkv * p.tiles;
+  const long long steps = (near + 1 < p.tiles ? near + 1 : p.tiles) * G;
+  p.parts = 1;
+  if (items < kItemsWanted && steps >= kStepsWorthParts) {
+    const long long n = (kItemsWanted + items - 1) / items;
+    p.parts = static_cast<int>(n < G ? n : G);
+  }
   p.sink_tiles = p.chunks = p.chunk_tiles = 0;
   if (far > 0 && s > 0) {
     const long long st = (s + kTile - 1) / kTile;
     p.sink_tiles = static_cast<int>(st < far ? st : far);  // tile t has far - t of them
-    long long n = (far + near) / (near + 1);
-    n = n < 1 ? 1 : (n > kMaxChunks ? kMaxChunks : n);
+    long long n = (far + near) / (near + 1) * p.parts;
+    n = n > kMaxChunks ? kMaxChunks : (n > far ? far : n);
     p.chunk_tiles = static_cast<int>((far + n - 1) / n);
     p.chunks = static_cast<int>((far + p.chunk_tiles - 1) / p.chunk_tiles);
   }
+  p.part_tiles = p.parts > 1 ? p.tiles : p.sink_tiles;
   const size_t rows = static_cast<size_t>(B) * H * N;
   p.d_bytes = (rows * 4 + 255) / 256 * 256;
-  p.part_bytes = static_cast<size_t>(B) * Hkv * p.sink_tiles * (1 + p.chunks) * 2 * kTile * d * 4;
+  p.part_bytes = static_cast<size_t>(B) * Hkv * p.part_tiles * (p.parts + p.chunks) * 2 * kTile * d * 4;
   return p;
 }
 
@@ -1015,9 +1042,9 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   d.H = a.H;
   d.N = a.N;
   const long long per = 8 * (32 / (D / 8)) * kDotRows, blocks = (d.rows + per - 1) / per;
-  const long long kv_items = static_cast<long long>(a.B) * a.Hkv * (a.tiles + static_cast<long long>(a.sink_tiles) * a.chunks);
+  const long long kv_items = static_cast<long long>(a.B) * a.Hkv * (static_cast<long long>(a.tiles) * a.parts + static_cast<long long>(a.sink_tiles) * a.chunks);
   const long long q_items = static_cast<long long>(a.B) * a.H * a.tiles;
-  const long long sink_elems = static_cast<long long>(a.B) * a.Hkv * a.sink_tiles * 2 * kTile * (D / 4);
+  const long long sink_elems = static_cast<long long>(a.B) * a.Hkv * a.part_tiles * 2 * kTile * (D / 4);
   if (blocks > 0x7fffffffLL || kv_items > 0x7fffffffLL || q_items > 0x7fffffffLL || sink_elems / 256 > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;
   dot_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(d);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
@@ -1049,8 +1076,8 @@ int launch(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_vi
   if (kv_items + runs > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
   kernel<<<static_cast<unsigned>(kv_items + runs), kThreads, smem, s>>>(mq, mk, mv, mo, kv, qa);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  if (a.sink_tiles > 0) {
-    sink_kernel<D><<<static_cast<unsigned>((sink_elems + 255) / 256), 256, 0, s>>>(kv);
+  if (a.part_tiles > 0) {
+    sum_kernel<D><<<static_cast<unsigned>((sink_elems + 255) / 256), 256, 0, s>>>(kv);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   }
   return BSA_OK;
@@ -1105,6 +1132,8 @@ extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const b
   a.sink_tiles = p.sink_tiles;
   a.chunks = p.chunks;
   a.chunk_tiles = p.chunk_tiles;
+  a.parts = p.parts;
+  a.part_tiles = p.part_tiles;
   a.scale = scale;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -163,3 +163,13 @@ def test_gradients_do_not_move_with_what_is_not_seen(H, Hkv, d, window, sinks):
         x[:, :, :cut] *= 1e6
     for a, b in zip(run(large[0], k, v, large[1])[1:], first[1:]):
         assert torch.equal(a[:, :, cut:], b[:, :, cut:])
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,window,sinks,lens", [
+    (1, 12, 1, 1100, 300, 0, None), (1, 7, 1, 1600, 200, 5, None), (2, 9, 3, 777, 5000, 3, [500, 777]),
+    (1, 3, 1, 4100, 130, 140, None)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_with_few_key_tiles_and_many_heads(B, H, Hkv, N, window, sinks, lens, d):
+    """Groups whose heads are cut into parts, evenly or not, whose sums are added up."""
+    q, k, v, do = make(B, H, Hkv, N, d, 29)
+    check(run(q, k, v, do, window, sinks, lens), exact(q, k, v, do, window, sinks, d ** -0.5, lens), d ** -0.5)
