@@ -88,6 +88,7 @@ struct Args {
   unsigned pairs;     // items per tile row of a cached head (G even: G / 2; else G)
   unsigned rows;      // tile rows: q tiles (G even) or pairs of them
   int by_head;        // the two slots are two heads
+  int rows_first;     // items go through all heads of a tile row before the next row
   int wide;           // O's rows are 32-byte aligned
   int window, sinks;
   unsigned items;
@@ -105,12 +106,16 @@ struct Item {
   }
 };
 
+// Items run from the last tile row, which sees the most keys, to the first.
 __device__ __forceinline__ Item item_of(const Args& a, unsigned i) {
   Item it;
   unsigned r = i / a.pairs;
   const int p = static_cast<int>(i - r * a.pairs);
-  i = r / a.rows;
-  const int row = static_cast<int>(r - i * a.rows);
+  const unsigned by = a.rows_first ? a.Hkv * a.B : a.rows;
+  i = r / by;
+  r -= i * by;
+  const int row = static_cast<int>(a.rows - 1 - (a.rows_first ? i : r));
+  if (a.rows_first) i = r;
   it.b = static_cast<int>(i / a.Hkv);
   it.hk = static_cast<int>(i - it.b * a.Hkv);
   it.h0 = it.hk * a.G + (a.by_head ? 2 * p : p);
@@ -126,9 +131,16 @@ __device__ __forceinline__ Item item_of(const Args& a, unsigned i) {
   return it;
 }
 
-// The next item from i on (by the grid's stride) that has steps; false: none.
+// A block's next item: a wave of the grid takes them in turn, the next one backward,
+// so that who had the longest of one wave has the shortest of the next.
+__device__ __forceinline__ unsigned after(unsigned i) {
+  const unsigned n = gridDim.x, w = i / n;
+  return (w + 1) * n + (n - 1 - (i - w * n));
+}
+
+// The next item from i on that has steps; false: none.
 __device__ __forceinline__ bool seek(const Args& a, unsigned& i, Item& it) {
-  for (; i < a.items; i += gridDim.x) {
+  for (; i < a.items; i = after(i)) {
     it = item_of(a, i);
     if (it.steps > 0) return true;
   }
@@ -153,7 +165,7 @@ __device__ void load_role(const CUtensorMap* mq, const CUtensorMap* mk, const CU
   const int lane = threadIdx.x & 31;
   uint32_t n = 0, items = 0, fixes = 0;
   bool ok = true;
-  for (unsigned i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+  for (unsigned i = blockIdx.x; i < a.items && ok; i = after(i)) {
     const Item it = item_of(a, i);
     if (it.steps == 0) continue;
     for (int s = 0; s < kSlots && ok; ++s) {
@@ -323,7 +335,7 @@ __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t 
       ok = mma_step<D, false>(tmem, sbase, ctl, lead, n, j == 0, narrow_step(a, it, j), true,
                               narrow_step(a, it, j + 1), j + 2 == it.steps);
     const bool one = it.steps == 1, narrow = narrow_step(a, it, it.steps - 1);
-    i += gridDim.x;
+    i = after(i);
     have = seek(a, i, it);
     ok = ok && mma_step<D, true>(tmem, sbase, ctl, lead, n, one, narrow, have, have && narrow_step(a, it, 0),
                                  have && it.steps == 1);
@@ -490,7 +502,7 @@ __device__ __forceinline__ void store_half_row(const Rest& r, float inv, uint32_
 // up a wait: the slot's other warps count on it there, and barriers have no limit.
 // Its vote is yes, so all take the barriers of a raise.
 __device__ __noinline__ void keep_step(int s, const Args& a, unsigned i, int j, bool pending) {
-  for (; i < a.items; i += gridDim.x, j = 0) {
+  for (; i < a.items; i = after(i), j = 0) {
     const Item it = item_of(a, i);
     for (; j < it.steps; ++j) {
       slot_vote(s, true);
@@ -535,7 +547,7 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
     rest.pending = false;
     return true;
   };
-  for (unsigned i = blockIdx.x; i < a.items; i += gridDim.x) {
+  for (unsigned i = blockIdx.x; i < a.items; i = after(i)) {
     const Item it = item_of(a, i);
     const int q0 = it.q0(s), q = q0 + row;
     float m = -INFINITY, l = 0.f;  // maximum (log2 units) of the row, sum of this thread's columns
@@ -711,6 +723,9 @@ extern "C" int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bs
   a.pairs = a.by_head ? a.G / 2 : a.G;
   a.rows = a.by_head ? tiles : (tiles + 1) / 2;
   a.window = window < N ? window : N;
+  // Rows first balances the blocks where rows differ (the longest items begin first), as
+  // long as what a row of all heads sees stays in half of L2 until the next row.
+  a.rows_first = static_cast<long long>(B) * Hkv * (a.window + 2 * kTile) * d * 4 <= (64LL << 20);
   a.sinks = sinks < N ? sinks : N;
   const long long items = static_cast<long long>(B) * Hkv * a.rows * a.pairs;
   if (items >= (1LL << 31)) return BSA_ERR_UNSUPPORTED;
