@@ -131,16 +131,18 @@ __device__ __forceinline__ Item item_of(const Args& a, unsigned i) {
   return it;
 }
 
-// A block's next item: a wave of the grid takes them in turn, the next one backward,
-// so that who had the longest of one wave has the shortest of the next.
-__device__ __forceinline__ unsigned after(unsigned i) {
-  const unsigned n = gridDim.x, w = i / n;
+// A block's next item.  Rows first, a wave of the grid takes them in turn and the next
+// one backward, so that who had the longest of one wave has the shortest of the next.
+__device__ __forceinline__ unsigned after(const Args& a, unsigned i) {
+  const unsigned n = gridDim.x;
+  if (!a.rows_first) return i + n;
+  const unsigned w = i / n;
   return (w + 1) * n + (n - 1 - (i - w * n));
 }
 
 // The next item from i on that has steps; false: none.
 __device__ __forceinline__ bool seek(const Args& a, unsigned& i, Item& it) {
-  for (; i < a.items; i = after(i)) {
+  for (; i < a.items; i = after(a, i)) {
     it = item_of(a, i);
     if (it.steps > 0) return true;
   }
@@ -165,7 +167,7 @@ __device__ void load_role(const CUtensorMap* mq, const CUtensorMap* mk, const CU
   const int lane = threadIdx.x & 31;
   uint32_t n = 0, items = 0, fixes = 0;
   bool ok = true;
-  for (unsigned i = blockIdx.x; i < a.items && ok; i = after(i)) {
+  for (unsigned i = blockIdx.x; i < a.items && ok; i = after(a, i)) {
     const Item it = item_of(a, i);
     if (it.steps == 0) continue;
     for (int s = 0; s < kSlots && ok; ++s) {
@@ -335,7 +337,7 @@ __device__ void mma_role(const Args& a, unsigned char* smem, Ctl* ctl, uint32_t 
       ok = mma_step<D, false>(tmem, sbase, ctl, lead, n, j == 0, narrow_step(a, it, j), true,
                               narrow_step(a, it, j + 1), j + 2 == it.steps);
     const bool one = it.steps == 1, narrow = narrow_step(a, it, it.steps - 1);
-    i = after(i);
+    i = after(a, i);
     have = seek(a, i, it);
     ok = ok && mma_step<D, true>(tmem, sbase, ctl, lead, n, one, narrow, have, have && narrow_step(a, it, 0),
                                  have && it.steps == 1);
@@ -502,7 +504,7 @@ __device__ __forceinline__ void store_half_row(const Rest& r, float inv, uint32_
 // up a wait: the slot's other warps count on it there, and barriers have no limit.
 // Its vote is yes, so all take the barriers of a raise.
 __device__ __noinline__ void keep_step(int s, const Args& a, unsigned i, int j, bool pending) {
-  for (; i < a.items; i = after(i), j = 0) {
+  for (; i < a.items; i = after(a, i), j = 0) {
     const Item it = item_of(a, i);
     for (; j < it.steps; ++j) {
       slot_vote(s, true);
@@ -547,7 +549,7 @@ __device__ void softmax_role(int s, const Args& a, Ctl* ctl, uint32_t tmem) {
     rest.pending = false;
     return true;
   };
-  for (unsigned i = blockIdx.x; i < a.items; i = after(i)) {
+  for (unsigned i = blockIdx.x; i < a.items; i = after(a, i)) {
     const Item it = item_of(a, i);
     const int q0 = it.q0(s), q = q0 + row;
     float m = -INFINITY, l = 0.f;  // maximum (log2 units) of the row, sum of this thread's columns

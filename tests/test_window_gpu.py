@@ -159,3 +159,21 @@ def test_forward_does_not_move_with_what_is_not_seen(Hkv, d):
             x[:, :, hidden] *= 1e6
         got, other = bsa.window_forward(q, *far, 100, 0)
         assert torch.equal(got[:, :, rows], first[:, :, rows]) and torch.equal(other[:, :, rows], lse[:, :, rows])
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,d,window", [(2, 6, 2, 4000, 64, 4000), (2, 12, 6, 2900, 128, 2000), (40, 8, 8, 900, 128, 900)])
+def test_forward_with_several_waves_of_unequal_tiles(B, H, Hkv, N, d, window):
+    """More tiles than SMs and rows that see more and more keys, in both orders of the
+    items (few heads: all heads of a row in turn; many: one head after another)."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v = (torch.randn(B, h, N, d, generator=g, device="cuda").to(torch.bfloat16) for h in (H, Hkv, Hkv))
+    got, lse = bsa.window_forward(q, k, v, window, 3)
+    assert bsa.stream_status() == 0
+    i = torch.arange(N, device="cuda")
+    seen = (i <= i[:, None]) & ((i > i[:, None] - window) | (i < 3))
+    for b in range(0, B, max(1, B // 3)):
+        for h in range(H):
+            x = (q[b, h].double() @ k[b, h * Hkv // H].double().T * d ** -0.5).masked_fill(~seen, -torch.inf)
+            want = torch.softmax(x, -1) @ v[b, h * Hkv // H].double()
+            torch.testing.assert_close(got[b, h].double(), want, rtol=2.0 ** -8, atol=2.0 ** -8 * 6)  # |v| below 6
+            torch.testing.assert_close(lse[b, h].double(), torch.logsumexp(x, -1), rtol=0, atol=2.0 ** -12)
