@@ -30,12 +30,13 @@
 // more than 2^20), 2^x with the scale folded in.  P is rounded to bf16 (2^-8 at most, like the
 // operands it meets); maxima, sums and O are fp32.
 //
-// Measured, 32 heads over 8, 32768 x 128, window 1024, 4 sinks: 0.70 ms, 770
+// Measured, 32 heads over 8, 32768 x 128, window 1024, 4 sinks: 0.71 ms, 760
 // TFLOP/s of visible pairs.  Two 128 x 128 tiles with their softmax take 1.93 us on
 // an SM (1.58 with the softmax left out), so the hand-over between products and
 // exponentials is what bounds it.  One thread per row, with 128 scores, took
-// 1.05 ms (spills), with 64 at a time 0.88; a lane that walked the steps alone
-// 0.79, as its operands then left the uniform registers.
+// 1.05 ms (spills), with 64 at a time 0.88; two threads a row and products whose
+// operands stay in uniform registers 0.81; the next item's first S issued early, sinks
+// last and few raises the rest.
 //
 // Every wait is bounded.
 #include "bsa_window.cuh"
