@@ -61,6 +61,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxM = 4096;
 constexpr float kRescale = 8.f;  // log2 units by which a maximum must grow to be raised
+// Maxima begin at the least finite number: weights are then 0 for scores of -inf, NaN for
+// NaN (which no comparison sees, but every sum keeps) and at most 1 for any other.
+constexpr float kLeast = -3.402823466e38f;
 
 __device__ unsigned int g_sdec_status;
 
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      w.top[nt][j] = -INFINITY;
+      w.top[nt][j] = kLeast;
       w.sum[nt][j] = 0.f;
 #pragma unroll
       for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] = 0.f;
@@ -779,7 +782,6 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // the maximum is finite: every unit shows a key
           const float p = ex2(x[s][nt][i] - w.top[nt][i & 1]);
           x[s][nt][i] = p;
           w.sum[nt][i & 1] += p;
@@ -825,30 +827,28 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
         }
     }
   __syncthreads();
+  const bool none = sp.units == 0;  // no rows are seen
+  auto finish = [&](int e, int head, float o, float sum, float top) {
+    a.O[head0 * D + e] = __float2bfloat16_rn(none ? 0.f : o / sum);
+    if (e % D == 0) a.LSE[head0 + head] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  };
   float* out = reinterpret_cast<float*>(smem + C::SMEM - C::OUT);
   const float* parts = reinterpret_cast<const float*>(smem);
   constexpr int PS = C::HEADS * (D + 2);
   for (int e = tid; e < heads * D; e += C::THREADS) {
     const int head = e / D;
-    float top = -INFINITY;
+    float top = kLeast;
 #pragma unroll
     for (int v = 0; v < NW; ++v) top = fmaxf(top, parts[v * PS + C::HEADS * D + head]);
     float o = 0.f, sum = 0.f;
-    if (top != -INFINITY) {
 #pragma unroll
-      for (int v = 0; v < NW; ++v) {
-        const float m = parts[v * PS + C::HEADS * D + head];
-        if (m != -INFINITY) {
-          const float f = ex2(m - top);
-          o = fmaf(parts[v * PS + e], f, o);
-          sum = fmaf(parts[v * PS + C::HEADS * D + C::HEADS + head], f, sum);
-        }
-      }
+    for (int v = 0; v < NW; ++v) {
+      const float f = ex2(parts[v * PS + C::HEADS * D + head] - top);
+      o = fmaf(parts[v * PS + e], f, o);
+      sum = fmaf(parts[v * PS + C::HEADS * D + C::HEADS + head], f, sum);
     }
     if (a.cluster == 1) {
-      a.O[head0 * D + e] = __float2bfloat16_rn(top == -INFINITY ? 0.f : o / sum);
-      if (e % D == 0)
-        a.LSE[head0 + head] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      finish(e, head, o, sum, top);
     } else {
       out[e] = o;
       if (e % D == 0) {
@@ -863,22 +863,16 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
   const int n = a.cluster;
   for (int e = rank * C::THREADS + tid; e < heads * D; e += n * C::THREADS) {
     const int head = e / D;
-    float top = -INFINITY;
+    float top = kLeast;
     for (int v = 0; v < n; ++v) top = fmaxf(top, cluster.map_shared_rank(out, v)[C::HEADS * D + head]);
     float o = 0.f, sum = 0.f;
-    if (top != -INFINITY)
-      for (int v = 0; v < n; ++v) {
-        const float* q = cluster.map_shared_rank(out, v);
-        const float m = q[C::HEADS * D + head];
-        if (m != -INFINITY) {
-          const float f = ex2(m - top);
-          o = fmaf(q[e], f, o);
-          sum = fmaf(q[C::HEADS * D + C::HEADS + head], f, sum);
-        }
-      }
-    a.O[head0 * D + e] = __float2bfloat16_rn(top == -INFINITY ? 0.f : o / sum);
-    if (e % D == 0)
-      a.LSE[head0 + head] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    for (int v = 0; v < n; ++v) {
+      const float* q = cluster.map_shared_rank(out, v);
+      const float f = ex2(q[C::HEADS * D + head] - top);
+      o = fmaf(q[e], f, o);
+      sum = fmaf(q[C::HEADS * D + C::HEADS + head], f, sum);
+    }
+    finish(e, head, o, sum, top);
   }
   cluster.sync();  // no CTA leaves while another reads its result
 }

@@ -436,7 +436,8 @@ int bsa_q4_read(const bsa_q4_cache* cache, const int32_t* start, const int32_t* 
  * q: device bf16 [B, H, d]; k_new, v_new: device bf16 [B, Hkv, d] or both NULL.
  * With them the step first puts the new token into cached row t (quantised for
  * a 4-bit cache) and attends to it as cached; else row t must hold it.  Cached
- * rows that are not visible may hold anything: they never reach the result.
+ * rows that are not visible may hold anything: they never reach the result.  Of
+ * rows that are, a score of -inf has weight 0 and one of NaN makes O and LSE NaN.
  * seq_len: device int32 [B] in 0..L (0: an empty entry, nothing appended);
  * others set BSA_STATUS_BAD_SEQ_LEN and count as 0.  O: bf16 [B, H, d]; LSE:
  * fp32 [B, H].  16-byte aligned (LSE 4).  One launch, enqueued on `stream`;

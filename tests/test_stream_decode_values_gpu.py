@@ -1,0 +1,102 @@
+"""Decode steps over long caches on values at the edges: NaN and infinite scores in
+rows that are seen, against the fp64 oracle.
+
+Tolerances as in test_stream_decode_gpu.py: |O - exact| <= 2^-8 |O| + 2^-10 max|v|
+(one bf16 rounding; weights to 2^-11 each, and the scores' fp32 error), LSE to 2^-13.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_38_b200 as bsa
+from oracle import long_stream as o
+
+from test_stream_decode_gpu import _make, _pack
+
+pytestmark = pytest.mark.gpu
+
+# (rows of the cache): one CTA a cached head, and a cluster of them
+LENGTHS = [70, 6000]
+
+
+def _step(bits, q, k, v, lens, window, sinks, new=None):
+    """Kernel and oracle on the same rows; the rows that the oracle reads."""
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = {} if new is None else dict(k_new=new[0].cuda(), v_new=new[1].cuda())
+    if bits == 4:
+        got = bsa.q4_window_decode(q.cuda(), _pack(k, v), seq, window, sinks, **kw)
+    else:
+        got = bsa.window_decode(q.cuda(), k.cuda(), v.cuda(), seq, window, sinks, **kw)
+    assert bsa.stream_status() == 0
+    if new is not None:
+        k, v = k.clone(), v.clone()
+        for b, n in enumerate(lens):
+            k[b, :, n - 1], v[b, :, n - 1] = new[0][b], new[1][b]
+    if bits == 4:
+        k, v = o.values(*o.quantise(k)), o.values(*o.quantise(v))
+    with np.errstate(invalid="ignore"):
+        want = o.decode(q, k, v, lens, lambda b, h, t: o.window_rows(t, window, sinks), q.shape[2] ** -0.5)
+    return [x.float().cpu().numpy() for x in got], want
+
+
+def _close(got, want, vmax=5.0):
+    np.testing.assert_allclose(got[0], want[0], rtol=2.0 ** -8 + 2.0 ** -20, atol=2.0 ** -10 * vmax)
+    np.testing.assert_allclose(got[1], want[1], rtol=2.0 ** -20, atol=2.0 ** -13)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("L", LENGTHS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_in_a_query_is_its_head_s_result(bits, L, d):
+    q, k, v, _, _ = _make(2, 2, 4, L, d, 41)
+    q[0, 5, 3] = float("nan")
+    q[1, 0] = float("nan")
+    got, want = _step(bits, q, k, v, [L, L - 5], L, 0)
+    assert np.isnan(want[0][0, 5]).all() and np.isnan(want[1][1, 0]) and np.isnan(want[0]).sum() == 2 * d
+    _close(got, want)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("L", LENGTHS)
+@pytest.mark.parametrize("where", ["alone in its unit", "only key", "new token alone in its unit", "a far warp's"])
+def test_a_nan_key_that_is_seen_is_not_dropped(bits, L, where):
+    q, k, v, kn, vn = _make(1, 1, 3, L, 128, 42)
+    window, sinks, new, n = L, 0, None, L
+    if where == "alone in its unit":  # rows 0 .. 32 are seen: row 32 begins a unit of either cache
+        n = 33
+        k[0, 0, 32, 7] = float("nan")
+    elif where == "only key":
+        window = 1
+        k[0, 0, L - 1, 7] = float("nan")
+    elif where == "new token alone in its unit":
+        n, new = 65, (kn, vn)
+        kn[0, 0, 9] = float("nan")
+    else:
+        k[0, 0, L // 2, 100] = float("nan")
+    got, want = _step(bits, q, k, v, [n], window, sinks, new)
+    assert np.isnan(want[0]).all() and np.isnan(want[1]).all()
+    _close(got, want)
+
+
+@pytest.mark.parametrize("L", LENGTHS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_score_of_minus_infinity_weighs_nothing(L, d):
+    """Keys with -inf in a channel where every query is positive, in whole units and in
+    a part of one; the weights of all other keys are as if these were not seen."""
+    q, k, v, _, _ = _make(2, 2, 4, L, d, 43)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[0, 0, :16, 0] = k[0, 1, 5:40, 0] = k[1, :, 48:68, 0] = k[1, :, 0, 0] = -float("inf")
+    got, want = _step(16, q, k, v, [L, L - 1], L, 0)
+    assert np.isfinite(want[0]).all() and np.isfinite(want[1]).all()
+    _close(got, want)
+
+
+@pytest.mark.parametrize("L", LENGTHS)
+def test_only_scores_of_minus_infinity(L):
+    """The sum of weights is 0: LSE = ln 0, and O = 0 / 0."""
+    q, k, v, _, _ = _make(1, 1, 4, L, 64, 44)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[..., 0] = -float("inf")
+    got = bsa.window_decode(q.cuda(), k.cuda(), v.cuda(), torch.tensor([L], dtype=torch.int32, device="cuda"), L)
+    assert bsa.stream_status() == 0
+    assert bool(torch.isnan(got[0]).all()) and bool(torch.isneginf(got[1]).all())
