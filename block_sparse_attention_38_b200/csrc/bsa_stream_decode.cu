@@ -23,10 +23,13 @@
 // add m_kG sum_{c in G} q_c by a product of their own, the sum in two fp16 terms
 // (2^-22).  For V, P^T is multiplied by the key's scale of
 // the group before its rounding to fp16 (2^-11, against 2^-8 of the bf16
-// output), and sum_k p_k m_kG is kept in fp32.  So that small or large scales
-// lose nothing to fp16's range, the running maximum is that of x_k + E - 6, with
-// 2^E the largest scale seen (E only grows, like a maximum); it is raised only by
-// more than 2^8, so P times a scale stays below 2^15.
+// output), and sum_k p_k m_kG is kept in fp32.  fp16's range is centred for each
+// group G: scales count in units of 2^E_G, which has been above every scale of the
+// group so far (E_G only grows, like a maximum, and is taken off at the join), and
+// the running maximum lies 2^6 below the largest weight.  It is raised only by
+// more than 2^8, so P times a scale stays below 2^15; and as fp16 goes down to
+// 2^-24, a weight is off by 2^-11, or by 2^-30 of the largest weight where that is
+// more, in units of the largest scale that the group has among the rows seen.
 //
 // bf16: operands by ldmatrix; P is split into two bf16 terms (P = hi + lo), so its
 // rounding costs 2^-16; the second product is free under the cache's bytes.
@@ -64,6 +67,7 @@ constexpr float kRescale = 8.f;  // log2 units by which a maximum must grow to b
 // Maxima begin at the least finite number: weights are then 0 for scores of -inf, NaN for
 // NaN (which no comparison sees, but every sum keeps) and at most 1 for any other.
 constexpr float kLeast = -3.402823466e38f;
+constexpr float kLift = 6.f;  // 4 bits: the weight of the running maximum, log2
 
 __device__ unsigned int g_sdec_status;
 
@@ -228,11 +232,10 @@ struct Warp {
   using C = Cfg<D, Q4, NT, NW>;
   // S^T columns 2t, 2t + 1 are this lane's heads in S and O
   float o[D / 16][NT][4];
-  float top[NT][2];      // running maximum, log2 units (shifted by E - 6 for 4 bits)
+  float top[NT][2];      // running maximum, log2 units (less kLift for 4 bits)
   float sum[NT][2];      // this lane's share of the denominator
   float pm[Q4 ? C::GR : 1][NT][2];  // sum_k p_k m_kG, this lane's keys
-  int e;                 // exponent of the largest value scale seen
-  float shift;           // E - 6 (4 bits), or 0
+  float unit[Q4 ? C::GR : 1];       // 2^-E_G
   uint32_t qf[NT][D / 16][2];
   uint32_t qs[NT][2];    // 2^-4 sum of q over group t, head g: high and low term, behind a 0
   float mul[NT][2];      // from accumulator to x in log2 units
@@ -495,10 +498,11 @@ __device__ __forceinline__ void value_tile(Warp<D, Q4, NT, NW>& w, const unsigne
       const uint32_t e = __byte_perm(vw[0][G / 2], vw[1][G / 2], sel), e8 = e >> 8;  // keys of rows 2t, 2t + 1
       const uint32_t f = __byte_perm(vw[2][G / 2], vw[3][G / 2], sel), f8 = f >> 8;  // the same + 8
       const float2 s0 = half2_of(vp[0][G]), s1 = half2_of(vp[1][G]);
+      const float u0 = s0.x * w.unit[G], u1 = s1.x * w.unit[G];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t b0 = transpose8x8(pack_h(p[nt][0] * s0.x, p[nt][1] * s0.x));
-        const uint32_t b1 = transpose8x8(pack_h(p[nt][2] * s1.x, p[nt][3] * s1.x));
+        const uint32_t b0 = transpose8x8(pack_h(p[nt][0] * u0, p[nt][1] * u0));
+        const uint32_t b1 = transpose8x8(pack_h(p[nt][2] * u1, p[nt][3] * u1));
         mma_f16(w.o[2 * G][nt], e & 0x000f000fu, e8 & 0x000f000fu, f & 0x000f000fu, f8 & 0x000f000fu, b0, b1);
         mma_f16(w.o[2 * G + 1][nt], e & 0x00f000f0u, e8 & 0x00f000f0u, f & 0x00f000f0u, f8 & 0x00f000f0u, b0, b1);
 #pragma unroll
@@ -645,8 +649,8 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
 #pragma unroll
       for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.pm[G][nt][j] = 0.f;
     }
-  w.e = -100;
-  w.shift = 0.f;
+#pragma unroll
+  for (int G = 0; G < (Q4 ? C::GR : 1); ++G) w.unit[G] = 0x1p25f;  // any scale above 0 calls for another
 #pragma unroll
   for (int m = 0; m < D / 16; ++m)
 #pragma unroll
@@ -728,16 +732,14 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
           }
         }
     }
-    // The running maximum (and E) are raised only where a lane's own scores (or
+    // The running maximum (and E_G) are raised only where a lane's own scores (or
     // scales) call for it, by more than the threshold: mostly one vote is all.
     bool want = false;
-    uint32_t big = 0u;
+    constexpr float kUp = Q4 ? kLift : 0.f;
+    const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + C::VP_OFF + lane * C::PROW);
     if constexpr (Q4) {
-      const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + C::VP_OFF + lane * C::PROW);
 #pragma unroll
-      for (int G = 0; G < C::GR; ++G) big = __vmaxu2(big, vp[G]);
-      big &= 0x7fffu;
-      want = static_cast<int>(big >> 10) - 15 > w.e;
+      for (int G = 0; G < C::GR; ++G) want |= half2_of(vp[G]).x * w.unit[G] >= 2.f;
     }
     float most[NT][2];
 #pragma unroll
@@ -748,13 +750,28 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
 #pragma unroll
         for (int s = 1; s < C::SUB; ++s) m = fmaxf(m, fmaxf(x[s][nt][j], x[s][nt][2 + j]));
         most[nt][j] = m;
-        want |= m + w.shift > w.top[nt][j] + kRescale;
+        want |= m > w.top[nt][j] + (kRescale + kUp);
       }
     if (__any_sync(0xffffffffu, want)) {
       if constexpr (Q4) {
-        big = __reduce_max_sync(0xffffffffu, big);
-        w.e = max(w.e, static_cast<int>(big >> 10) - 15);
-        w.shift = static_cast<float>(w.e - 6);
+#pragma unroll
+        for (int G = 0; G < C::GR; ++G) {
+          // E_G is one more than the largest scale's exponent: the next power of two is no cause to raise
+          const uint32_t big = min(__reduce_max_sync(0xffffffffu, vp[G] & 0x7fffu), 0x7bffu);
+          const float half_of = __half2float(__ushort_as_half(static_cast<unsigned short>(big)));
+          const float unit = __uint_as_float((253u << 23) - (__float_as_uint(half_of) & 0x7f800000u));
+          if (big != 0u && unit < w.unit[G]) {
+            const float f = unit * __uint_as_float((254u << 23) - __float_as_uint(w.unit[G]));
+            w.unit[G] = unit;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                w.o[2 * G][nt][i] *= f;
+                w.o[2 * G + 1][nt][i] *= f;
+              }
+          }
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -763,7 +780,7 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
           float m = most[nt][j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const float old = w.top[nt][j], now = fmaxf(old, m + w.shift);
+          const float old = w.top[nt][j], now = fmaxf(old, m - kUp);
           const float f = now == old ? 1.f : ex2(old - now);
           w.top[nt][j] = now;
           w.sum[nt][j] *= f;
@@ -822,7 +839,8 @@ __global__ void __launch_bounds__(32 * NW, Cfg<D, Q4, NT, NW>::PER_SM) stream_de
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float v = w.o[m][nt][2 * i + j];
-          if constexpr (Q4) v = fmaf(v, (m & 1) ? 0x1p20f : 0x1p24f, pm[m >> 1]);
+          if constexpr (Q4)  // 2^24 (or 2^20: the code was 16-fold) 2^E_G
+            v = fmaf(v, __uint_as_float(((m & 1) ? 274u << 23 : 278u << 23) - __float_as_uint(w.unit[m >> 1])), pm[m >> 1]);
           part[head * D + channel_of<D, Q4>(m, i, g)] = v;
         }
     }

@@ -100,3 +100,40 @@ def test_only_scores_of_minus_infinity(L):
     got = bsa.window_decode(q.cuda(), k.cuda(), v.cuda(), torch.tensor([L], dtype=torch.int32, device="cuda"), L)
     assert bsa.stream_status() == 0
     assert bool(torch.isnan(got[0]).all()) and bool(torch.isneginf(got[1]).all())
+
+
+@pytest.mark.parametrize("peaks,bits", [(1, 15), (256, 10), (256, 13)])
+@pytest.mark.parametrize("G,d,append", [(1, 64, False), (4, 128, True), (12, 128, False)])
+def test_channel_groups_of_unlike_scales_over_a_long_tail(G, d, append, peaks, bits):
+    """Value groups whose scales lie 2^10 to 2^22 apart, and keys (one, or one in each
+    warp's first rows) that outweigh each other one 2^bits times: each group keeps the
+    accuracy that it has alone, so the tolerance takes max|v| of the group."""
+    L, ratio = 40000, (0, -22, -20, -10)
+    g = torch.Generator().manual_seed(45)
+    q = torch.ones(1, G, d, dtype=torch.bfloat16)
+    k = (torch.randn(1, 1, L, d, generator=g) * 0.05).to(torch.bfloat16)
+    k[0, 0, 7:32 * peaks:32] = bits * np.log(2) / d ** 0.5
+    v = torch.randn(1, 1, L, d, generator=g)
+    for i in range(d // 32):
+        v[..., 32 * i:32 * i + 32] *= 2.0 ** ratio[i]
+    v = v.to(torch.bfloat16)
+    new = (k[:, :, 5].clone(), v[:, :, 5].clone()) if append else None
+    got, want = _step(4, q, k, v, [L], L, 0, new)
+    for i in range(d // 32):
+        at = slice(32 * i, 32 * i + 32)
+        _close((got[0][..., at], got[1]), (want[0][..., at], want[1]), 5 * 2.0 ** ratio[i])
+
+
+def test_a_group_whose_scale_grows_along_the_cache():
+    """One group's scale grows 2^20-fold row by row, another's falls so, a third has none."""
+    L, d = 9000, 128
+    g = torch.Generator().manual_seed(46)
+    q, k, v, _, _ = _make(1, 1, 4, L, d, 46)
+    grow = 2.0 ** torch.linspace(-10, 10, L)[:, None]
+    v = v.float()
+    v[0, 0, :, :32] *= grow
+    v[0, 0, :, 32:64] /= grow
+    v[0, 0, :, 64:96] = 3.0
+    got, want = _step(4, q, k, v.to(torch.bfloat16), [L], L, 0)
+    for at, vmax in ((slice(0, 64), 5 * 2.0 ** 10), (slice(64, 96), 3.0), (slice(96, 128), 5.0)):
+        _close((got[0][..., at], got[1]), (want[0][..., at], want[1]), vmax)
