@@ -137,3 +137,15 @@ def test_a_group_whose_scale_grows_along_the_cache():
     got, want = _step(4, q, k, v.to(torch.bfloat16), [L], L, 0)
     for at, vmax in ((slice(0, 64), 5 * 2.0 ** 10), (slice(64, 96), 3.0), (slice(96, 128), 5.0)):
         _close((got[0][..., at], got[1]), (want[0][..., at], want[1]), vmax)
+
+
+@pytest.mark.parametrize("B,Hkv,G,L,d,window,sinks,append", [
+    (1, 1, 4, 20000, 64, 20000, 0, True), (1, 1, 8, 40000, 128, 40000, 0, False), (1, 1, 1, 33333, 128, 30000, 7, True),
+    (2, 8, 4, 12000, 128, 12000, 0, False), (2, 4, 7, 17001, 64, 16900, 33, True)])
+def test_long_caches(B, Hkv, G, L, d, window, sinks, append):
+    """10 to 40 thousand visible rows of few heads, where clusters are cut off at 16 CTAs
+    and blocks of sixteen warps take over; lengths from 3 tokens to all."""
+    q, k, v, kn, vn = _make(B, Hkv, G, L, d, 47)
+    for lens in ([L, 3][:B], [L - 4999, L][:B]):
+        got, want = _step(4, q, k, v, lens, window, sinks, (kn, vn) if append else None)
+        _close(got, want)
