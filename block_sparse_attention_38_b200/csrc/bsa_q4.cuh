@@ -63,15 +63,15 @@ __device__ __forceinline__ Params group_params(float lo, float hi) {
   return p;
 }
 
-// floor((x - m) / s + 1/2), clamped to 0..15, as a float.  The quotient is taken
-// with a reciprocal that is high by 2^-20, so the rounded code is right or one
-// too high; the remainder x - m - code * s, which is exact (x has 8 bits, s and
-// m have 11), tells which.  An infinite or NaN quotient ends at a clamp.
+// floor((x - m) / s + 1/2), clamped to 0..15, as a float.  The quotient is taken with
+// a reciprocal that is high by 2^-20, so the rounded code c is right or one too high;
+// a comparison with the bound (c - 1/2) s, which is exact (5 bits times 11), tells
+// which.  The difference t = x - m is rounded down: bounds are fp32 numbers, so x - m
+// reaches one if and only if t does.  An infinite or NaN quotient ends at a clamp.
 __device__ __forceinline__ float code_of(float x, const Params& p) {
-  const float t = x - p.m;
+  const float t = __fsub_rd(x, p.m);
   float c = __fadd_rd(fmaf(t, p.inv, 0.5f), 12582912.f) - 12582912.f;  // floor
-  const float r = fmaf(-c, p.s, t);
-  if (r < -p.half) c -= 1.f;
+  if (t < fmaf(c, p.s, -p.half)) c -= 1.f;
   return fminf(fmaxf(c, 0.f), 15.f);
 }
 

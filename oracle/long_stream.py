@@ -32,8 +32,13 @@ def quantise(x):
         scale = np.where(wide > 65504, np.float32(65504), wide).astype(np.float16)
         least = np.clip(lo, -65504, 65504).astype(np.float16)
         s, m = scale.astype(np.float64)[..., None], least.astype(np.float64)[..., None]
-        code = np.floor((x - m) / np.where(s > 0, s, 1.0) + 0.5)
-        code = np.where(s > 0, np.clip(code, 0, 15), 0.0)
+        t = x - m
+        y = t - x
+        low = (x - (t - y)) - (m + y)  # x - m = t + low exactly
+        code = np.clip(np.floor(t / np.where(s > 0, s, 1.0) + 0.5), 0, 15)
+        bound = (code - 0.5) * s       # exact: 5 bits times 11
+        code -= (code > 0) & ((t < bound) | ((t == bound) & (low < 0)))
+        code = np.where(s > 0, code, 0.0)
     return code.reshape(code.shape[:-2] + (code.shape[-2] * GROUP,)).astype(np.uint8), scale, least
 
 
