@@ -50,7 +50,7 @@ struct Params {
 
 __device__ __forceinline__ Params group_params(float lo, float hi) {
   Params p;
-  float s = __fdiv_rn(hi - lo, 15.f);
+  float s = hi == lo ? 0.f : __fdiv_rn(hi - lo, 15.f);  // one infinity less another like it is no NaN
   s = s > kHalfMax ? kHalfMax : s;                       // a NaN stays
   float m = lo > kHalfMax ? kHalfMax : lo;
   m = m < -kHalfMax ? -kHalfMax : m;

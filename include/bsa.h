@@ -375,7 +375,8 @@ int bsa_decode_status(uint32_t* status, int clear);
  * s = fp16((max - min) / 15) and a minimum m = fp16(min), the quotient taken in
  * fp32 and both limited to +-65504, and a code floor((x - m) / s + 1/2) in 0..15
  * for each channel (0 where s is 0); it reads back as code * s + m.  A group
- * that holds a NaN reads back as NaN; an infinity is limited like the rest.
+ * that holds a NaN reads back as NaN; an infinity is limited like the rest, also in
+ * a group of infinities of one sign (max - min counts as 0).
  *
  * k_codes, v_codes: device bytes [B, H, L, d/2]; k_params, v_params: device
  * fp16 [B, H, L, d/32, 2] (scale, minimum); all contiguous, 16-byte aligned,

@@ -28,7 +28,7 @@ def quantise(x):
     x = x.reshape(x.shape[:-1] + (x.shape[-1] // GROUP, GROUP))
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         lo, hi = x.min(-1), x.max(-1)
-        wide = (hi.astype(np.float32) - lo.astype(np.float32)) / np.float32(15)
+        wide = np.where(hi == lo, np.float32(0), (hi.astype(np.float32) - lo.astype(np.float32)) / np.float32(15))
         scale = np.where(wide > 65504, np.float32(65504), wide).astype(np.float16)
         least = np.clip(lo, -65504, 65504).astype(np.float16)
         s, m = scale.astype(np.float64)[..., None], least.astype(np.float64)[..., None]

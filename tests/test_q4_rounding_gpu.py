@@ -54,3 +54,21 @@ def test_values_of_all_sizes_in_one_group(d):
     x[::2] = torch.round(x[::2] * 4) / 4 + torch.where(torch.rand(2000, d, generator=g) < 0.3, -2.0 ** -50, 0.0)
     x = x.to(torch.bfloat16)
     _check_rows(_written(x, x.flip(0), False), 0, 0, slice(0, 4000), x, x.flip(0))
+
+
+@pytest.mark.parametrize("append", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_group_of_infinities_is_limited_like_one_of_them(d, append):
+    x = torch.randn(4, d, generator=torch.Generator().manual_seed(52))
+    x[0, :32] = float("inf")
+    x[1, 32:64] = -float("inf")
+    x[2, :32], x[2, 5] = float("inf"), -float("inf")
+    x[3, :32], x[3, 7] = -float("inf"), 1.0
+    x = x.to(torch.bfloat16)
+    cache = _written(x, -x, append)
+    k, v = bsa.q4_read(cache, torch.zeros(1, dtype=torch.int32, device="cuda"), 4)
+    top = torch.tensor(65504.0).to(torch.bfloat16)     # rounds to 2^16
+    assert bool((k[0, 0, 0, :32].cpu() == top).all()) and bool((k[0, 0, 1, 32:64].cpu() == -top).all())
+    assert bool((v[0, 0, 0, :32].cpu() == -top).all()) and bool((v[0, 0, 1, 32:64].cpu() == top).all())
+    assert bool(torch.isfinite(k).all()) and bool(torch.isfinite(v).all())
+    _check_rows(cache, 0, 0, slice(0, 4), x, -x)
