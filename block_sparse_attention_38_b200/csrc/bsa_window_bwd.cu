@@ -21,7 +21,8 @@
 // (fp32), and one more product in each query tile takes it off again, spread evenly
 // over the keys of the diagonal tile that the query sees (the diagonal tile's own
 // errors over those of the same 32): that is exact for the offset, and leaves of each
-// error its product with the key's distance from its neighbours' mean.
+// error its product with the key's distance from its neighbours' mean.  The diagonal
+// tile comes last, after the sinks' (whose weights are the largest) and the window's.
 //
 // In both, sixteen warps (four threads a row) turn S into P (phase A), then dP
 // into dS (phase B), while the tensor core works on the products of the other
@@ -573,9 +574,9 @@ struct QCtl {
 
 struct QItem {
   int b, h, hk, q0, len;
-  int near, first, steps;  // the window's tiles, then the sinks'
+  int sunk, first, steps;  // the sinks' tiles, then the window's, of which the diagonal one is the last
   __device__ __forceinline__ int key0(int j) const {
-    return (j < near ? first + j : j - near) * kTile;
+    return (j < sunk ? j : first + j - sunk) * kTile;
   }
 };
 
@@ -590,8 +591,8 @@ __device__ __forceinline__ QItem q_item(const Args& a, unsigned i) {
   it.h = it.hk * a.G + g;
   it.len = length_of(a.lens, it.b, a.N, &g_wbwd_status);
   it.first = max(0, it.q0 - a.window + 1) / kTile;
-  it.near = (min(it.q0 + kTile, it.len) - 1) / kTile - it.first + 1;
-  it.steps = it.q0 < it.len ? it.near + min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first) : 0;
+  it.sunk = min((min(a.sinks, it.len) + kTile - 1) / kTile, it.first);
+  it.steps = it.q0 < it.len ? it.sunk + (min(it.q0 + kTile, it.len) - 1) / kTile - it.first + 1 : 0;
   return it;
 }
 
@@ -626,7 +627,7 @@ struct QWalk {
   __device__ __forceinline__ bool last() const { return j + 1 == it.steps; }
   // a sink tile outside the window that shows at most 32 keys takes 32 columns
   __device__ __forceinline__ bool narrow(const Args& a) const {
-    return j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
+    return j < it.sunk && a.sinks - j * kTile <= 32;
   }
 };
 
@@ -763,8 +764,8 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       return true;
     };
     // One step, with the next one's S before its dS is waited for.
-    auto step = [&](uint32_t t, int n, bool first, bool narrow, bool level, bool last, bool more, int nn, bool nfirst,
-                    bool nnarrow, bool nlast) {
+    auto step = [&](uint32_t t, int n, bool first, bool narrow, bool last, bool more, int nn, bool nfirst, bool nnarrow,
+                    bool nlast) {
       const int s = t & 1, buf = n & 1;
       if (first && !arrived(&ctl->do_full, n & 1)) return false;
       if (!arrived(&ctl->v_full[s], (t >> 1) & 1)) return false;
@@ -779,7 +780,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       if (!arrived(&ctl->ds_ready, t & 1)) return false;
       if (lead) {
         mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP, k + s * C::TILE, narrow, !first);
-        if (level) mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP + 16, k + s * C::TILE, false, true);
+        if (last) mma_ts<D>(tm + T_DQ + buf * D, tm + T_DP + 16, k + s * C::TILE, false, true);
         umma_commit(&ctl->k_empty[s]);
         if (last) umma_commit(&ctl->dq_full[buf]);
       }
@@ -795,11 +796,11 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         const bool narrow = w.narrow(a), first = w.j == 0;
         QWalk nx = w;
         ++nx.j;
-        ok = step(t, n, first, narrow, nx.j == w.it.near, false, true, n, false, nx.narrow(a), nx.j + 1 == steps);
+        ok = step(t, n, first, narrow, false, true, n, false, nx.narrow(a), nx.j + 1 == steps);
       }
-      const bool one = steps == 1, narrow = w.narrow(a), level = w.j + 1 == w.it.near;
+      const bool one = steps == 1, narrow = w.narrow(a);
       w.next(a);
-      ok = ok && step(t, n, one, narrow, level, true, w.valid, n + 1, true, w.valid && w.narrow(a), w.valid && w.last());
+      ok = ok && step(t, n, one, narrow, true, w.valid, n + 1, true, w.valid && w.narrow(a), w.valid && w.last());
       ++t;
     }
     if (lead) {
@@ -852,7 +853,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
       float off = 0.f;  // sum of dS's rounding errors over this thread's keys, before the diagonal tile and in it
       for (int j = 0; j < it.steps && ok; ++j, ++t) {
         const int kw = it.key0(j) + 32 * part;  // this thread's first key
-        const bool narrow = j >= it.near && a.sinks - (j - it.near) * kTile <= 32;
+        const bool narrow = j < it.sunk && a.sinks - j * kTile <= 32;
         // whether no row of the warp sees any of the 32 keys, or every row all of them
         const bool none = (narrow && part > 0) || kw > qw + 31 || (qw - (kw + 31) >= a.window && kw >= a.sinks);
         const bool all = kw + 31 <= qw && qw + 32 <= it.len && (qw + 31 - kw < a.window || kw + 32 <= a.sinks);
@@ -902,17 +903,17 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& mq, const CUtensorMa
         } else if (!narrow) {
           zero16(t_dp);
         }
-        if (j >= it.near - 2 && j < it.near) {
+        if (j >= it.steps - 2) {
           int r = row, c0 = 32 * part;
           asm volatile("" : "+r"(r), "+r"(c0));  // what follows is computed here, not kept from the loop's start
-          if (j == it.near - 2) {  // read at the next step, written again only after that step's ds_ready
+          if (j == it.steps - 2) {  // read at the next step, written again only after that step's ds_ready
             ctl->off[c0 >> 5][r] = off;
             off = 0.f;
           } else {  // the diagonal tile: its key of column c is q - r + c
             const int lo = max(0, r - a.window + 1), below = min(max(a.sinks - q + r, 0), lo);
             const uint32_t seen = upto(r + 1 - c0) & (~upto(lo - c0) | upto(below - c0));
             float share = seen ? __fdividef(-off, static_cast<float>(__popc(seen))) : 0.f;
-            if (it.near > 1) {
+            if (it.steps > 1) {
               // this step's dP was issued after the last step's ds_ready of all warps: this
               // is true at once, and orders their writes before the reads
               mbar_try_wait(&ctl->ds_ready, (t - 1) & 1);
