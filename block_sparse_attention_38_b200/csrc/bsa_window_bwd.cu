@@ -59,7 +59,8 @@ struct Args {
   __nv_bfloat16* out[2];     // dV, dK, or dQ
   long long sb[2], sh[2], sn[2];
   int wide[2];               // the outputs' rows are 32-byte aligned
-  float* part;               // [B * Hkv, part tiles, parts + chunks, 2, 128, d]
+  float* part;               // partial sums, fp32: [B * Hkv, part tiles, parts, 2, 128, d]
+  float* far_part;           // and of far queries [B * Hkv, sink tiles, chunks, 2, 128, d]
   int B, H, N;
   unsigned Hkv, G, tiles;
   int window, sinks;
@@ -203,12 +204,14 @@ struct KvCtl {
 };
 
 struct KvItem {
-  int b, hk, kt, k0, len, slot;      // slot: the partial result's place, or -1
+  int b, hk, kt, k0, len;
+  float* part;                       // the partial result's place (row 0 of dV), or null
   int g0, heads;                     // the group's heads that it takes
   bool far;
   int first, count;                  // query tiles
 };
 
+template <int D>
 __device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
   KvItem it;
   const unsigned main_items = static_cast<unsigned>(a.B) * a.Hkv * a.tiles * a.parts;
@@ -242,11 +245,13 @@ __device__ __forceinline__ KvItem kv_item(const Args& a, unsigned i) {
   if (!it.far) {
     it.first = it.kt;
     end = min(near, last);
-    it.slot = it.kt < static_cast<int>(a.part_tiles) ? static_cast<int>(part) : -1;
+    it.part = it.kt < static_cast<int>(a.part_tiles)
+                  ? a.part + ((static_cast<long long>(bh) * a.part_tiles + it.kt) * a.parts + part) * (2 * kTile * D)
+                  : nullptr;
   } else {
     it.first = near + 1 + chunk * a.chunk_tiles;
     end = min(it.first + a.chunk_tiles - 1, last);
-    it.slot = static_cast<int>(a.parts) + chunk;
+    it.part = a.far_part + ((static_cast<long long>(bh) * a.sink_tiles + it.kt) * a.chunks + chunk) * (2 * kTile * D);
   }
   it.count = it.k0 < it.len ? max(0, end - it.first + 1) : 0;
   return it;
@@ -261,7 +266,7 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
   unsigned char *sK = smem, *sV = smem + C::TILE, *sQ = smem + 2 * C::TILE, *sO = smem + 4 * C::TILE;
   KvCtl* ctl = reinterpret_cast<KvCtl*>(smem + 6 * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const KvItem it = kv_item(a, item);
+  const KvItem it = kv_item<D>(a, item);
   const int G = it.heads, steps = it.count * G, head0 = it.hk * static_cast<int>(a.G) + it.g0;
 
   if (tid == 0) {
@@ -499,13 +504,12 @@ __device__ __forceinline__ void dkdv_item(const CUtensorMap& mq, const CUtensorM
         const uint32_t t_acc = t_lane + (w == 0 ? T_DV : T_DK) + c0;
         const float mul = w == 0 ? 1.f : a.scale;
         const bool zero = none || (w == 1 && a.alone);
-        if (it.slot < 0) {
+        if (it.part == nullptr) {
           __nv_bfloat16* dst = a.out[w] + it.b * a.sb[w] + it.hk * a.sh[w] + static_cast<long long>(k) * a.sn[w] + c0;
 #pragma unroll 1
           for (int c = 0; c < D / 4; c += 16) store_row16(t_acc + c, mul, zero, dst + c, k < a.N, a.wide[w]);
         } else if (!idle) {
-          const long long tile = (static_cast<long long>(it.b) * a.Hkv + it.hk) * a.part_tiles + it.kt;
-          float* dst = a.part + (((tile * (a.parts + a.chunks) + it.slot) * 2 + w) * kTile + row) * D + c0;
+          float* dst = it.part + (w * kTile + row) * D + c0;
 #pragma unroll 1
           for (int c = 0; c < D / 4; c += 16) {
             float x[16];
@@ -546,16 +550,20 @@ __global__ void __launch_bounds__(256) sum_kernel(const Args a) {
   const int kt = static_cast<int>(tile % a.part_tiles), k = kt * kTile + row;
   if (k >= a.N) return;
   const long long bh = tile / a.part_tiles;
-  const int n = static_cast<int>(a.parts + (kt < static_cast<int>(a.sink_tiles) && k < a.sinks ? a.chunks : 0u));
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < n; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(
-        a.part + (((tile * (a.parts + a.chunks) + i) * 2 + w) * kTile + row) * D + 4 * c);
-    s.x += x.x;
-    s.y += x.y;
-    s.z += x.z;
-    s.w += x.w;
-  }
+  auto add = [&](const float* from, unsigned n) {
+    from += (w * kTile + row) * D + 4 * c;
+    for (unsigned i = 0; i < n; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(from + static_cast<long long>(i) * (2 * kTile * D));
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+  };
+  add(a.part + tile * a.parts * (2 * kTile * D), a.parts);
+  if (kt < static_cast<int>(a.sink_tiles) && k < a.sinks)
+    add(a.far_part + (bh * a.sink_tiles + kt) * a.chunks * (2 * kTile * D), a.chunks);
   const int b = static_cast<int>(bh / a.Hkv), hk = static_cast<int>(bh % a.Hkv);
   *reinterpret_cast<uint2*>(a.out[w] + b * a.sb[w] + hk * a.sh[w] + static_cast<long long>(k) * a.sn[w] + 4 * c) =
       make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
@@ -982,7 +990,8 @@ constexpr int kItemsWanted = 60, kStepsWorthParts = 8;
 
 struct Plan {
   int tiles, sink_tiles, chunks, chunk_tiles, parts, part_tiles;
-  size_t d_bytes, part_bytes;
+  size_t d_bytes, part_bytes, far_bytes;
+  size_t bytes() const { return d_bytes + part_bytes + far_bytes; }
 };
 
 Plan make_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
@@ -1011,7 +1020,9 @@ Plan make_plan(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   p.part_tiles = p.parts > 1 ? p.tiles : p.sink_tiles;
   const size_t rows = static_cast<size_t>(B) * H * N;
   p.d_bytes = (rows * 4 + 255) / 256 * 256;
-  p.part_bytes = static_cast<size_t>(B) * Hkv * p.part_tiles * (p.parts + p.chunks) * 2 * kTile * d * 4;
+  const size_t sums = static_cast<size_t>(B) * Hkv * 2 * kTile * d * 4;  // dV and dK of a tile for every head
+  p.part_bytes = sums * p.part_tiles * p.parts;
+  p.far_bytes = sums * p.sink_tiles * p.chunks;
   return p;
 }
 
@@ -1095,7 +1106,7 @@ int window_backward_status(uint32_t* status, int clear) {
 extern "C" size_t bsa_window_backward_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || N < 1 || (d != 64 && d != 128) || window < 1 || sinks < 0) return 0;
   const auto p = bsa::wbwd::make_plan(B, H, Hkv, N, d, window, sinks);
-  return p.d_bytes + p.part_bytes;
+  return p.bytes();
 }
 
 extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const bsa_view* v, const bsa_view* o,
@@ -1114,12 +1125,13 @@ extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const b
   if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
   if (N > (1 << 30)) return BSA_ERR_UNSUPPORTED;
   const Plan p = make_plan(B, H, Hkv, N, d, window, sinks);
-  if (workspace_bytes < p.d_bytes + p.part_bytes) return BSA_ERR_BUFFER_TOO_SMALL;
+  if (workspace_bytes < p.bytes()) return BSA_ERR_BUFFER_TOO_SMALL;
   Args a = {};
   a.lens = lens;
   a.LSE = LSE;
   a.Dq = static_cast<float*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.d_bytes);
+  a.far_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.d_bytes + p.part_bytes);
   a.B = B;
   a.H = H;
   a.Hkv = Hkv;
