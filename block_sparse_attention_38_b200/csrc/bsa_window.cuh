@@ -105,8 +105,8 @@ inline bool make_map(CUtensorMap* m, const bsa_view* v, int B, int H, int N, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A view a tensor map can describe, and whose rows do not overlap: aligned, with
-// every stride that is used a positive multiple of 8 below 2^39.
+// A view that a tensor map can describe: aligned, with every stride that is used a
+// multiple of 8, at least d and below 2^39.
 inline bool view_ok(const bsa_view* v, int B, int H, int N, int d) {
   if (!v || !v->data || (reinterpret_cast<uintptr_t>(v->data) & 15u) != 0) return false;
   const int64_t s[3] = {v->stride_b, v->stride_h, v->stride_n};
@@ -114,6 +114,24 @@ inline bool view_ok(const bsa_view* v, int B, int H, int N, int d) {
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (s[i] < d || s[i] % 8 != 0 || s[i] >= (1LL << 39))) return false;
   return true;
+}
+
+// Whether rows of a view may overlap, which one to be written must not: taken from the
+// smallest stride to the largest, each must pass all that the ones before it span.
+inline bool rows_overlap(const bsa_view* v, int B, int H, int N, int d) {
+  const int64_t s[3] = {v->stride_b, v->stride_h, v->stride_n};
+  int n[3] = {B, H, N};
+  unsigned __int128 span = static_cast<unsigned>(d);  // (2^30 - 1) 2^39 is past 64 bits
+  for (int i = 0; i < 3; ++i) {
+    int at = -1;
+    for (int j = 0; j < 3; ++j)
+      if (n[j] > 1 && (at < 0 || s[j] < s[at])) at = j;
+    if (at < 0) break;
+    if (static_cast<uint64_t>(s[at]) < span) return true;
+    span += static_cast<unsigned __int128>(n[at] - 1) * static_cast<uint64_t>(s[at]);
+    n[at] = 1;
+  }
+  return false;
 }
 
 inline int sm_count() {

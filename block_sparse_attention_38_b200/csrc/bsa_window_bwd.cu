@@ -1126,6 +1126,8 @@ extern "C" int bsa_window_backward(const bsa_view* q, const bsa_view* k, const b
   if (N > (1 << 30)) return BSA_ERR_UNSUPPORTED;
   const Plan p = make_plan(B, H, Hkv, N, d, window, sinks);
   if (workspace_bytes < p.bytes()) return BSA_ERR_BUFFER_TOO_SMALL;
+  if (rows_overlap(dq, B, H, N, d) || rows_overlap(dk, B, Hkv, N, d) || rows_overlap(dv, B, Hkv, N, d))
+    return BSA_ERR_INVALID_ARG;
   Args a = {};
   a.lens = lens;
   a.LSE = LSE;

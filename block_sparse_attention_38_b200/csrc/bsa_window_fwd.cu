@@ -708,6 +708,7 @@ extern "C" int bsa_window_forward(const bsa_view* q, const bsa_view* k, const bs
     return BSA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
   if (N > (1 << 30)) return BSA_ERR_UNSUPPORTED;
+  if (rows_overlap(o, B, H, N, d)) return BSA_ERR_INVALID_ARG;
   Args a = {};
   a.lens = lens;
   a.O = static_cast<__nv_bfloat16*>(const_cast<void*>(o->data));

@@ -470,7 +470,8 @@ int bsa_window_decode(const void* q, const void* k_new, const void* v_new, void*
  * up to 255 tokens before it or 384 past its window and, where its 128-row tile
  * holds sinks, every later one (their weight for it is 0, and 0 times NaN is not).
  * Strides (of dimensions of more than one entry): positive multiples of 8, at
- * least d, below 2^39.  Any N up to 2^30, any H / Hkv; d in {64, 128}.  One
+ * least d, below 2^39.  o's rows must not overlap: from the smallest of its strides
+ * to the largest, each is at least what the ones before it span.  Any N up to 2^30, any H / Hkv; d in {64, 128}.  One
  * launch, enqueued on `stream`; nothing allocated or synchronised; the same bits
  * every run.
  */

@@ -3,6 +3,9 @@ pointers are never used)."""
 import pytest
 
 import block_sparse_attention_38_b200 as bsa
+from block_sparse_attention_38_b200 import long_stream as ls
+
+P = 4096  # never used as a pointer
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -21,3 +24,17 @@ def test_backward_workspace_is_no_more_than_its_parts(B, H, Hkv, N, window, sink
     sunk = -(-min(sinks, N) // 128)
     most = B * H * N * 4 + 256 + B * Hkv * tile * ((tiles if parts > 1 else sunk) * parts + sunk * 32)
     assert B * H * N * 4 <= bsa.window_backward_workspace_bytes(B, H, Hkv, N, d, window, sinks) <= most
+
+
+# strides in units of d = 64 of [B, H, N] = [2, 6, 40]
+OVERLAPPING = [(2, 1, 1), (240, 1, 1), (1, 1, 6), (40, 40, 1), (240, 1, 5), (239, 40, 1), (120, 1, 2)]
+
+
+@pytest.mark.parametrize("strides", OVERLAPPING, ids=str)
+def test_outputs_whose_rows_overlap_are_refused(strides):
+    lib, sizes = bsa.library(), (2, 6, 6, 40, 64, 8, 2, 0.1)
+    bad, good = (ls._View(P, *(64 * s for s in x)) for x in (strides, (240, 40, 1)))
+    assert lib.bsa_window_forward(good, good, good, None, *sizes, bad, P, None) == bsa.ERR_INVALID_ARG
+    for at in range(3):
+        grads = [bad if i == at else good for i in range(3)]
+        assert lib.bsa_window_backward(*[good] * 5, P, None, *sizes, *grads, P, 1 << 30, None) == bsa.ERR_INVALID_ARG

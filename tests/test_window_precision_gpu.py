@@ -1,5 +1,6 @@
 """How exact the window kernels are where the wider bounds of their other tests would
-not tell: the LSE, and dQ over keys with an offset that all of them share."""
+not tell: the LSE, and dQ over keys with an offset that all of them share; and where
+they write."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +71,21 @@ def test_an_offset_of_all_keys_leaves_dq_exact(G, N, window, sinks, lens, d):
         far += ((dq[0, h, :n].double().cpu().numpy() - want) ** 2).sum()
         near += 2 * (ds ** 2 @ (size + size[sinks:].mean())).sum() + (want ** 2).sum()
     assert far <= 2.0 ** -16 * near, (far / near) ** 0.5 * 2 ** 8
+
+
+@pytest.mark.parametrize("strides", [(240, 40, 1), (240, 1, 6), (1, 80, 2), (1, 2, 12), (40, 80, 1), (5000, 3, 100),
+                                     (241, 40, 1)], ids=str)
+@pytest.mark.parametrize("dk", [0, 8])
+def test_an_out_in_any_order_of_its_dimensions(strides, dk):
+    """Rows of every order and spacing that do not overlap; the bytes between them stay."""
+    q, k, v, _ = (x.cuda() for x in make(2, 6, 3, 40, 64, 63))
+    want, lse = bsa.window_forward(q, k, v, 8, 2)
+    step = [(64 + dk) * s for s in strides]
+    whole = torch.full((sum((n - 1) * s for n, s in zip((2, 6, 40), step)) + 64 + 8,), 7.0, dtype=torch.bfloat16,
+                       device="cuda")
+    out = whole.as_strided((2, 6, 40, 64), (*step, 1))
+    got, other = bsa.window_forward(q, k, v, 8, 2, out=out)
+    assert bsa.stream_status() == 0
+    assert got is out and torch.equal(out, want) and torch.equal(other, lse)
+    out.fill_(7.0)
+    assert bool((whole == 7.0).all())
