@@ -15,9 +15,14 @@ library loads on a machine without a GPU (only compute calls need one).
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
+import runpy
 import subprocess
 import sys
+import sysconfig
+
+from .long_stream import marshal_tag
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,18 +57,38 @@ def stale(target=LIB, deps=None) -> bool:
     return any(os.path.getmtime(p) > t for p in (DEPS if deps is None else deps))
 
 
-def build_marshal(force: bool = False) -> str:
-    """_bsa_torch.so: torch is loaded only when it has to be built."""
-    if not force and not stale(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "bsa.h")]):
+def torch_home():
+    """Folder and version of the torch that this Python would import, without importing
+    it; (None, None) where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None, None
+    at = spec.submodule_search_locations[0]
+    return at, str(runpy.run_path(os.path.join(at, "version.py"))["__version__"])
+
+
+def marshal_stale(version: str) -> bool:
+    """Whether sources are newer than the module, or its file does not hold the text that
+    says what it was built for."""
+    if stale(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "bsa.h")]):
+        return True
+    with open(MARSHAL, "rb") as f:
+        return marshal_tag(version).encode() not in f.read()
+
+
+def build_marshal(force: bool = False):
+    """_bsa_torch.so, for the torch and Python at hand; None where there is no torch,
+    without which only the calls that take tensors are missing."""
+    at, version = torch_home()
+    if at is None:
+        print("no torch: _bsa_torch.so is not built", file=sys.stderr)
+        return None
+    if not force and not marshal_stale(version):
         return MARSHAL
-    import sysconfig
-
-    import torch
-
-    at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = MARSHAL + f".tmp{os.getpid()}"
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f'-DBSA_BUILT_FOR="{marshal_tag(version)}"',
                     "-I" + os.path.join(ROOT, "include"), "-I" + os.path.join(at, "include"),
                     "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), MARSHAL_SOURCE,
                     "-o", tmp, "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
@@ -73,13 +98,13 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """The library, which needs nvcc only, and then the binding's module."""
+    if force or stale():
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [NVCC] + FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + SOURCES + ["-o", tmp]
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
     build_marshal(force)
-    if not force and not stale():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC] + FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + SOURCES + ["-o", tmp]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
     return LIB
 
 

@@ -422,4 +422,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bsa_torch", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bsa_torch() { return PyModule_Create(&module); }
+// The torch and Python that this was built for, which the build gives.
+PyMODINIT_FUNC PyInit__bsa_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BSA_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

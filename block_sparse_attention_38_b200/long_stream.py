@@ -11,6 +11,7 @@ h // (H // Hkv).
 from __future__ import annotations
 
 import ctypes
+import sysconfig
 from typing import NamedTuple, Optional
 
 from . import _check, library  # defined before this module is imported
@@ -18,15 +19,24 @@ from . import _check, library  # defined before this module is imported
 _marshal = None  # csrc/bsa_torch.cpp, loaded by the first call that takes tensors: the package loads without torch
 
 
+def marshal_tag(torch_version: str) -> str:
+    """What _bsa_torch.so is built for; the module has it as a constant."""
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _load():
     global _marshal
-    import torch  # noqa: F401  (its libraries come first)
+    import torch  # its libraries come first
 
     try:
         from . import _bsa_torch as module
     except ImportError as e:
         raise ImportError(f"_bsa_torch.so is missing or does not load ({e}): build it with "
                           "`python -m block_sparse_attention_38_b200.build`") from e
+    made_for, here = getattr(module, "built_for", "an earlier version of this package"), marshal_tag(torch.__version__)
+    if made_for != here:
+        raise ImportError(f"_bsa_torch.so was built for {made_for}, not for {here}: build it with "
+                          "`python -m block_sparse_attention_38_b200.build`")
     lib = library()
     module.init(_check, *(ctypes.cast(getattr(lib, "bsa_" + name), ctypes.c_void_p).value for name in (
         "q4_write", "q4_read", "q4_decode", "q4_window_decode", "window_decode", "window_forward",
