@@ -377,6 +377,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError& e) {  // torch's own type, as its allocations raise it
+    const Owned torch(PyImport_ImportModule("torch"));
+    const Owned type(torch ? PyObject_GetAttrString(torch.get(), "OutOfMemoryError") : nullptr);
+    if (type) PyErr_SetString(type.get(), e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
