@@ -157,8 +157,13 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: Optional[float] 
     q: CUDA bf16 [B, H, N, d]; k, v: [B, Hkv, N, d]; any strides that are
     multiples of 8 with d contiguous and rows that do not overlap, so a
     sequence-major tensor is passed as its transpose(1, 2).  lens: CUDA int32
-    [B], tokens of each sequence (all N where None); rows past them give O = 0
-    and LSE = -inf.  Returns (O like q, LSE fp32 [B, H, N]).
+    [B], tokens of each sequence (all N where None); rows past them may hold
+    anything and give O = 0 and LSE = -inf.  Returns (O like q, LSE fp32 [B, H, N]).
+
+    A NaN or infinity in a value row inside its sequence can also reach queries
+    that do not see that row (their weight for it is 0, and 0 times NaN is NaN):
+    those up to 255 tokens before it or 384 past its window and, where its 128-row
+    tile holds sinks, every later one.
     """
     return (_marshal or _load()).window_forward(q, k, v, window, sinks, scale, lens, out, lse)
 
@@ -176,6 +181,9 @@ def window_backward(q, k, v, o, do, lse, window: int, sinks: int = 0, scale: Opt
     """Gradients of `window_forward` (bsa_window_backward): (dQ like q, dK like k,
     dV like v) for the gradient do of its output o; lse as it returned it (copied
     first where it is not contiguous).
+
+    A NaN or infinity inside a sequence can also reach gradients of rows up to 384
+    tokens from those that its row meets, and of 128-row tiles with sinks.
 
     workspace: a CUDA tensor of at least window_backward_workspace_bytes(...)
     bytes (allocated on the current stream when not given); calls that may run
